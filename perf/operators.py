@@ -246,7 +246,7 @@ def _plain(state):
     if state["op"] == "quantize":
         t = state["x_scale"]
         if state["matrix_scale"]:
-            t = (x.abs().max().float() / 2688).reshape(1)
+            t = (x.abs().max().double() / 2688).float().reshape(1)
         y = _quantized_values(x, fmt, t).to(x.dtype)
         return (y, t) if state["matrix_scale"] else (y,)
     v = x.float() if state["op"].endswith("gemv") else _quantized_values(x, fmt, state["x_scale"])
