@@ -32,7 +32,7 @@ def _sources():
 def _shared_inputs():
     """Files every translation unit depends on: the headers and this script."""
     return (sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
-            + [os.path.join(ROOT, "include", "lnq.h"), os.path.abspath(__file__)])
+            + sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)])
 
 
 def _obj(src: str) -> str:

@@ -23,7 +23,9 @@ cudaError_t fisher_syrk(const __nv_bfloat16 *X, const float *S, const float *M,
 
 static std::atomic<long long> g_wait_limit{kDefaultWaitLimit};
 
-static int device_sm_count()
+long long wait_limit() { return g_wait_limit.load(); }
+
+int device_sm_count()
 {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
