@@ -49,8 +49,10 @@ typedef enum { LNQ_FP4_MX = 0, LNQ_FP4_NV = 1 } lnq_fp4_format;
 /* Types of unquantised matrices. */
 typedef enum { LNQ_F32 = 0, LNQ_BF16 = 1, LNQ_F16 = 2 } lnq_dtype;
 
-/* Largest d and number of experts the operators take. */
+/* Largest sizes the operators take: elements of a row, rows of a matrix (of all experts' matrices
+ * together), experts. */
 #define LNQ_FP4_MAX_D (1ll << 24)
+#define LNQ_FP4_MAX_ROWS (1ll << 30)
 #define LNQ_FP4_MAX_EXPERTS 1024
 
 /* Bytes per row of codes and of scales (0 if d or fmt is invalid). */

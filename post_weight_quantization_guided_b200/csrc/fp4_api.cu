@@ -5,13 +5,12 @@
 namespace lnq {
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool valid_fmt(int fmt) { return fmt == LNQ_FP4_MX || fmt == LNQ_FP4_NV; }
 bool valid_type(int t) { return t == LNQ_F32 || t == LNQ_BF16 || t == LNQ_F16; }
 bool valid_d(int64_t d) { return d >= 1 && d <= LNQ_FP4_MAX_D; }
-bool valid_rows(int64_t n) { return n >= 0 && n <= kMaxRows; }
+bool valid_rows(int64_t n) { return n >= 0 && n <= LNQ_FP4_MAX_ROWS; }
 
 // An unquantised matrix of n rows and d columns.
 bool valid_dense(const void *p, int type, int64_t n, int64_t d, int64_t ld)
@@ -41,7 +40,7 @@ lnq_status status_of(cudaError_t e)
 bool valid_product(int64_t n, int64_t d_out, int64_t d_in, int64_t experts, int fmt)
 {
     return valid_rows(n) && valid_d(d_in) && valid_fmt(fmt) && d_out >= 1 && experts >= 1 &&
-           experts <= LNQ_FP4_MAX_EXPERTS && d_out <= kMaxRows && d_out * experts <= kMaxRows;
+           experts <= LNQ_FP4_MAX_EXPERTS && d_out <= LNQ_FP4_MAX_ROWS && d_out * experts <= LNQ_FP4_MAX_ROWS;
 }
 
 lnq_status gemv(const void *x, int xt, int64_t n, int64_t ldx, const int32_t *offsets,

@@ -1,100 +1,618 @@
 // fp4_gemm.cu -- the product of two quantised matrices, and the same with the rows grouped by
-// expert.
+// expert, on the block-scaled tensor cores.
 //
 //   y[b][j] = ta tw sum_i (code sa)[b][i] (code sw)[j][i]
 //
-// A CTA computes a 64 x 64 tile: it decodes 32 columns of both operands into shared memory at a
-// time, and each thread accumulates a 4 x 4 piece.
+// The weights are the MMA's M side (its rows are outputs j), the activations its N side, so that
+// few rows cost narrow tiles, not padded ones. A cluster pair of CTAs computes 256 outputs x BN
+// rows (BN = 32 .. 256) with tcgen05.mma.cta_group::2.kind::mxf4nvf4 (M = 256, N = BN, K = 64 per
+// instruction); each CTA holds its 128 outputs' codes and half of the BN rows' codes.
+//
+// Per stage of 256 elements of K, a CTA's shared memory takes
+//   - both operands' codes by TMA (128 bytes a row, 128-byte swizzle), zeros outside the matrix;
+//   - the block scales of its 128 outputs and of all BN rows, row-major in memory, by 4-byte
+//     asynchronous copies that put row r's four scales of 64 (NV) or 128 (MX) elements where the
+//     tensor core wants them: byte 16 (r % 32) + 4 (r / 32 % 4) of a 512-byte atom per 128 rows.
+// The MMA thread copies the atoms to TMEM (tcgen05.cp, 4 columns each, a slot per stage so that no
+// copy overtakes an MMA that still reads) and issues four MMAs. All K-wise bounds are in the
+// copies: codes and scales behind the row's end arrive as zeros.
+//
+// Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8-9 scales, 10 TMA,
+// 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs share the rows' tile.
+// With few tiles, `split` pairs of one cluster take a share of K each and add their sums through
+// distributed shared memory in a fixed order.
+#include <cstring>
+
 #include "fp4.cuh"
+#include "fp4_mma.cuh"
+#include "lnq_internal.cuh"
 #include "profile.cuh"
 
 namespace lnq {
 
 __device__ uint32_t g_fp4_error[2];
 
-constexpr int kTile = 64, kDepth = 32;
+namespace f4 {
+constexpr int BM = 128, PM = 256;       // outputs of a CTA, of a pair
+constexpr int BK = 256;                 // elements of K per stage: 128 bytes of codes a row
+constexpr int kEpiWarps = 8, kScaleWarps = 2;  // 12 warps in all: 168 registers a thread
+constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kScaleLag = 2;            // stages between a scale copy's issue and its hand-over
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxSplit = 4;            // pairs of a cluster
+constexpr int kAtom = 512;              // bytes of scales of 128 rows x 4 blocks
 
-template <int FMT>
-__device__ __forceinline__ void decode_tile(float (&out)[kDepth][kTile + 1], const Fp4Matrix &m,
-                                            int64_t first, int64_t behind, int64_t i0, int64_t d)
+template <int BN, int FMT>
+struct Tile {
+    static constexpr int kAtomsK = BK / fp4_block(FMT) / 4;       // scale atoms per stage along K
+    static constexpr int kAtomsN = (BN + 127) / 128;              // along the rows
+    static constexpr int kABytes = BM * 128, kBBytes = BN / 2 * 128;
+    static constexpr int kScaleBytes = kAtomsK * (1 + kAtomsN) * kAtom;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kSlotCols = kAtomsK * 4 * (1 + kAtomsN);  // TMEM columns of a stage's scales
+    static constexpr int kAcc = BN == 256 ? 1 : 2;                 // accumulators
+    static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 7 : 8);
+    static constexpr int kLimInts = LNQ_FP4_MAX_EXPERTS + 1;
+    static constexpr int kBars = 3 * kStages + 2 * kAcc + 1;
+    static constexpr size_t kSmem = static_cast<size_t>(kStages) * (kStageBytes + kScaleBytes) +
+                                    2 * kLimInts * 4 + kBars * 8 + 32 + 1024 /* alignment */;
+    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(kStages * kSlotCols + kAcc * BN <= static_cast<int>(kTmemCols), "TMEM");
+    static_assert(kStageBytes % 1024 == 0 && kStages > kScaleLag, "stages");
+    static_assert(BN > 128 || BN * BM * 4 <= kStages * kStageBytes, "partial sums of a split");
+};
+}  // namespace f4
+
+struct Fp4GemmParams {
+    const uint8_t *a_scales, *w_scales;  // rows (activations), outputs (weights)
+    const float *ta, *tw;
+    const int32_t *offsets;
+    void *y;
+    int64_t ldy;
+    int64_t w_total;       // outputs of all matrices
+    int n, experts, d_out;
+    int yt;
+    int nk;                // stages of K
+    int blocks;            // scale blocks of a row
+    int scale_pitch;       // bytes
+    int mt;                // output tiles of one matrix
+    int split;             // pairs that share a tile's K
+    long long limit;
+};
+
+template <typename T>
+__device__ __forceinline__ void store_column(T *__restrict__ y, int64_t ldy, int count,
+                                             const uint32_t (&v)[32], float ta, float tw)
 {
-    const int64_t padded = fp4_padded(d);
-    const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;  // 256 threads: 64 rows x 4 words
-    const int64_t row = first + r;
-    uint32_t word = 0u;
-    float s = 0.f;
-    if (row < behind && i0 + c < d) {
-        word = reinterpret_cast<const uint32_t *>(m.codes + row * (padded / 2))[(i0 + c) / 8];
-        s = fp4_scale_value<FMT>(
-            m.scales[row * (padded / fp4_block(FMT)) + (i0 + c) / fp4_block(FMT)]);
+    if (count >= 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            y[c * ldy] = from_f32<T>(__uint_as_float(v[c]) * ta * tw);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (c < count)
+                y[c * ldy] = from_f32<T>(__uint_as_float(v[c]) * ta * tw);
     }
-    for (int k = 0; k < 8; ++k)
-        out[c + k][r] = i0 + c + k < d ? fp4_code_value((word >> (4 * k)) & 15u) * s : 0.f;
 }
 
-template <typename TY, int FMT>
-__global__ void __launch_bounds__(256)
-    fp4_gemm_kernel(Fp4Matrix a, const int32_t *__restrict__ offsets, Fp4Matrix w, int64_t d_in,
-                    TY *__restrict__ y, int64_t ldy)
+// Where a tile lies: group, first row and the row behind the group's last, first output.
+struct Fp4TileAt {
+    int e, b0, b1, j0;
+};
+
+template <int BN>
+__device__ __forceinline__ Fp4TileAt tile_at(int64_t tile, const Fp4GemmParams &p, const int *lim,
+                                             const int *pre)
 {
-    __shared__ float as[kDepth][kTile + 1], bs[kDepth][kTile + 1];
-    const int e = blockIdx.z;
-    const int n = static_cast<int>(a.rows);
-    const int2 rows = offsets == nullptr ? make_int2(0, n) : fp4_group_rows(offsets, e, n);
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const float ta = a.t == nullptr ? 1.f : *a.t, tw = w.t == nullptr ? 1.f : w.t[e];
-    const int tr = (threadIdx.x >> 4) * 4, tc = (threadIdx.x & 15) * 4;
-    for (int64_t b0 = rows.x + static_cast<int64_t>(blockIdx.y) * kTile; b0 < rows.y;
-         b0 += static_cast<int64_t>(gridDim.y) * kTile) {
-        float acc[4][4] = {};
-        for (int64_t i0 = 0; i0 < d_in; i0 += kDepth) {
-            __syncthreads();
-            decode_tile<FMT>(as, a, b0, rows.y, i0, d_in);
-            decode_tile<FMT>(bs, w, e * w.rows + j0, (e + 1) * w.rows, i0, d_in);
-            __syncthreads();
-            for (int k = 0; k < kDepth; ++k)
-                for (int p = 0; p < 4; ++p)
-                    for (int q = 0; q < 4; ++q)
-                        acc[p][q] = fmaf(as[k][tr + p], bs[k][tc + q], acc[p][q]);
-        }
-        for (int p = 0; p < 4; ++p)
-            for (int q = 0; q < 4; ++q)
-                if (b0 + tr + p < rows.y && j0 + tc + q < w.rows)
-                    y[(b0 + tr + p) * ldy + j0 + tc + q] = from_f32<TY>(acc[p][q] * ta * tw);
+    const int q = static_cast<int>(tile / p.mt), m = static_cast<int>(tile - int64_t(q) * p.mt);
+    int lo = 0, hi = p.experts;  // pre[lo] <= q < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= q)
+            lo = mid;
+        else
+            hi = mid;
     }
+    return Fp4TileAt{lo, lim[lo] + (q - pre[lo]) * BN, lim[lo + 1], m * f4::PM};
+}
+
+template <int BN, int FMT>
+__global__ void __launch_bounds__(f4::kThreads, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
+                    const __grid_constant__ CUtensorMap amap, const Fp4GemmParams p)
+{
+    using namespace f4;
+    using T = Tile<BN, FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
+    uint8_t *sf = smem + T::kStages * T::kStageBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sf + T::kStages * T::kScaleBytes);
+    uint64_t *full = bars;                           // codes landed (leader's: both CTAs')
+    uint64_t *scaled = full + T::kStages;            // scales landed (leader's: both CTAs')
+    uint64_t *empty = scaled + T::kStages;           // stage and TMEM slot free (each CTA's)
+    uint64_t *tfull = empty + T::kStages;            // accumulator done (each CTA's)
+    uint64_t *tempty = tfull + T::kAcc;              // accumulator read (leader's: both CTAs')
+    uint64_t *drain = tempty + T::kAcc;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    int *lim = reinterpret_cast<int *>(tmem_holder + 4);  // [experts + 1] group boundaries
+    int *pre = lim + T::kLimInts;                         // [experts + 1] row tiles before group e
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank(), cr = rank & 1u, leader = rank & ~1u;
+    const int part = static_cast<int>(rank >> 1);          // this pair's share of K
+    const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
+    const int64_t first = blockIdx.x / (2 * p.split), step = gridDim.x / (2 * p.split);
+    const int kb0 = part * p.nk / p.split, kb1 = (part + 1) * p.nk / p.split;
+    DeviceErr err{g_fp4_error, p.limit};
+
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < T::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&scaled[s], 2 * kScaleWarps);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < T::kAcc; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], 2 * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        fence_barrier_init();
+        tma_prefetch_desc(&wmap);
+        tma_prefetch_desc(&amap);
+    }
+    if (warp == kMmaWarp)
+        tmem_alloc_pair(tmem_holder, kTmemCols);
+    if (warp == 0) {
+        // group boundaries: offsets limited to 0 .. n and to no less than the largest before
+        int top = 0, tiles = 0;
+        if (p.offsets == nullptr) {
+            if (lane < 2)
+                lim[lane] = lane * p.n;
+        } else {
+            for (int i = lane; i - lane <= p.experts; i += 32) {
+                int v = i <= p.experts ? min(p.offsets[i], p.n) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, v, o);
+                    v = lane >= o ? max(v, u) : v;
+                }
+                v = max(v, top);
+                top = __shfl_sync(0xffffffffu, v, 31);
+                if (i <= p.experts)
+                    lim[i] = v;
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            pre[0] = 0;
+        for (int i = lane; i - lane < p.experts; i += 32) {
+            int v = i < p.experts ? (lim[i + 1] - lim[i] + BN - 1) / BN : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                v += lane >= o ? u : 0;
+            }
+            v += tiles;
+            tiles = __shfl_sync(0xffffffffu, v, 31);
+            if (i < p.experts)
+                pre[i + 1] = v;
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    const int64_t num_tiles = static_cast<int64_t>(pre[p.experts]) * p.mt;
+
+    if (warp == kTmaWarp) {
+        // ------------------------------------------------------------------ codes by TMA
+        if (lane == 0) {
+            uint32_t fpar = 0u, fused = 0u;  // per stage: parity of the fills, ever filled
+            int stage = 0;
+            bool ok = true;
+            for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+                const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
+                const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
+                const int arow = at.b0 + static_cast<int>(cr) * (BN / 2);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&empty[stage], ((fpar >> stage) & 1u) ^ 1u, p.limit)) {
+                        raise_error(err, kErrTimeout, 1);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = smem + stage * T::kStageBytes;
+                    if (cr == 0)
+                        mbar_arrive_expect_tx(&full[stage], 2 * T::kStageBytes);
+                    const uint32_t fb = cluster_addr(&full[stage], leader);
+                    tma_load_2d_pair(st, &wmap, fb, kb * 128, wrow);
+                    tma_load_2d_pair(st + T::kABytes, &amap, fb, kb * 128, arow);
+                    fpar ^= 1u << stage;
+                    fused |= 1u << stage;
+                    stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                }
+            }
+            if (!ok) {
+                // let this CTA's copies land: the leader waits for the last fill of each stage;
+                // its peer's copies are counted there, so the peer waits a fixed time
+                if (cr == 0) {
+                    for (int s = 0; s < T::kStages; ++s)
+                        if ((fused >> s) & 1u)
+                            mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, 1LL << 22);
+                } else {
+                    const long long c0 = clock64();
+                    while (clock64() - c0 < (1LL << 22)) {
+                    }
+                }
+            }
+        }
+    } else if (warp >= kEpiWarps && warp < kTmaWarp) {
+        // ------------------------------------------------------------------ block scales
+        constexpr int kSpan = kScaleWarps * 32;      // rows that the threads take at a time
+        constexpr int kSetsW = BM / kSpan, kSets = kSetsW + (BN + kSpan - 1) / kSpan;
+        const int r = threadIdx.x - kEpiWarps * 32;
+        const uint32_t sf_base = smem_u32(sf);
+        const uint32_t scaled_leader = cluster_addr(&scaled[0], leader);
+        uint32_t fpar = 0u;
+        int stage = 0, issued = 0, given = 0, given_stage = 0;
+        bool ok = true;
+        auto hand_over = [&]() {  // this warp's copies of the oldest stage have landed
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(scaled_leader + static_cast<uint32_t>(given_stage * 8));
+            ++given;
+            given_stage = given_stage + 1 == T::kStages ? 0 : given_stage + 1;
+        };
+        for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+            const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
+            // sets of rows: this CTA's outputs, then the tile's rows. Rows outside the arrays (and
+            // those whose sums nobody reads) get zeros.
+            const uint8_t *src[kSets];
+            int blocks[kSets];
+#pragma unroll
+            for (int g = 0; g < kSets; ++g) {
+                const bool weights = g < kSetsW;
+                const int i = (weights ? g : g - kSetsW) * kSpan + r;
+                const int64_t row = weights ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
+                                                  static_cast<int>(cr) * BM + i
+                                            : static_cast<int64_t>(at.b0) + i;
+                const bool in = weights ? row < p.w_total : (i < BN && row < p.n);
+                src[g] = (weights ? p.w_scales : p.a_scales) + (in ? row : 0) * p.scale_pitch;
+                blocks[g] = in ? p.blocks : 0;
+            }
+            for (int kb = kb0; kb < kb1; ++kb) {
+                int got = 0;
+                if (lane == 0)
+                    got = mbar_wait(&empty[stage], ((fpar >> stage) & 1u) ^ 1u, p.limit) ? 1 : 0;
+                got = __shfl_sync(0xffffffffu, got, 0);
+                if (!got) {
+                    if (lane == 0)
+                        raise_error(err, kErrTimeout, 2);
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = sf_base + static_cast<uint32_t>(stage * T::kScaleBytes);
+#pragma unroll
+                for (int g = 0; g < kSets; ++g) {
+                    const bool weights = g < kSetsW;
+                    const int i = (weights ? g : g - kSetsW) * kSpan + r;
+                    const uint32_t at_atom = static_cast<uint32_t>((i & 31) * 16 + ((i >> 5) & 3) * 4);
+#pragma unroll
+                    for (int a = 0; a < T::kAtomsK; ++a) {
+                        const int k0 = (kb * T::kAtomsK + a) * 4;  // first block of the word
+                        const int atom = weights ? a : T::kAtomsK + a * T::kAtomsN + i / 128;
+                        const int bytes = min(max(blocks[g] - k0, 0), 4);
+                        if (weights || i < BN)
+                            cp_async4_zfill(dst + atom * kAtom + at_atom,
+                                            bytes > 0 ? src[g] + k0 : src[g],
+                                            static_cast<uint32_t>(bytes));
+                    }
+                }
+                cp_async_commit();
+                fpar ^= 1u << stage;
+                stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                if (++issued > kScaleLag) {
+                    cp_async_wait_group<kScaleLag>();
+                    hand_over();
+                }
+            }
+        }
+        cp_async_wait_all();
+        while (given < issued)
+            hand_over();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------------ MMA issue (leader)
+        if (cr == 0 && lane == 0) {
+            constexpr bool kNv = FMT == LNQ_FP4_NV;
+            int stage = 0, it = 0;
+            uint32_t fph = 0u;  // per stage: phase parity
+            bool ok = true;
+            for (int64_t tile = first; tile < num_tiles && ok; tile += step, ++it) {
+                const int acc = it % T::kAcc, use = it / T::kAcc;
+                if (!mbar_wait_cluster(&tempty[acc], (use & 1) ^ 1, p.limit)) {
+                    raise_error(err, kErrTimeout, 3);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&full[stage], (fph >> stage) & 1u, p.limit) ||
+                        !mbar_wait_cluster(&scaled[stage], (fph >> stage) & 1u, p.limit)) {
+                        raise_error(err, kErrTimeout, 4);
+                        ok = false;
+                        break;
+                    }
+                    fph ^= 1u << stage;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * T::kStageBytes);
+                    const uint32_t sb = sa + T::kABytes;
+                    const uint32_t ss = smem_u32(sf + stage * T::kScaleBytes);
+                    const uint32_t slot =
+                        tmem_base + static_cast<uint32_t>(T::kAcc * BN + stage * T::kSlotCols);
+#pragma unroll
+                    for (int c = 0; c < T::kAtomsK * (1 + T::kAtomsN); ++c)
+                        tmem_cp_32x128b_pair(slot + c * 4, smem_desc_plain(ss + c * kAtom));
+#pragma unroll
+                    for (int kk = 0; kk < BK / 64; ++kk) {
+                        const int atom = kNv ? kk : kk / 2;
+                        const uint32_t idesc = umma_idesc_f4(PM, BN, !kNv, kNv ? 0u : (kk & 1) * 2u);
+                        const uint64_t ad = umma_desc_sw128(sa + kk * 32, 16, 1024);
+                        const uint64_t bd = umma_desc_sw128(sb + kk * 32, 16, 1024);
+                        umma_f4_pair<kNv>(d_tmem, ad, bd, idesc, slot + atom * 4,
+                                          slot + (T::kAtomsK + atom * T::kAtomsN) * 4,
+                                          (kb != kb0 || kk != 0) ? 1u : 0u);
+                    }
+                    umma_commit_pair(&empty[stage], pair_mask);
+                    stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                }
+                if (!ok)
+                    break;
+                umma_commit_pair(&tfull[acc], pair_mask);
+            }
+            // every MMA of this thread has completed once `drain` flips
+            umma_commit_pair(drain, static_cast<uint16_t>(1u << leader));
+            mbar_wait(drain, 0, kDrainLimit);
+        }
+    } else {
+        // ------------------------------------------------------------------ epilogue
+        constexpr int kChunks = (BN / 32 + 1) / 2;  // 32-column chunks of a warp
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t tempty_leader = cluster_addr(&tempty[0], leader);
+        const float ta = p.ta == nullptr ? 1.f : __ldg(p.ta);
+        int it = 0;
+        for (int64_t tile = first; tile < num_tiles; tile += step, ++it) {
+            const int acc = it % T::kAcc, use = it / T::kAcc;
+            int ok = 0;
+            if (lane == 0)
+                ok = mbar_wait(&tfull[acc], use & 1, p.limit) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) {
+                if (lane == 0)
+                    raise_error(err, kErrTimeout, 5);
+                break;
+            }
+            __syncwarp();
+            tc_fence_after();
+            const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                   static_cast<uint32_t>(acc * BN);
+            const int rows = min(at.b1 - at.b0, BN);  // rows of this tile
+            // the accumulator is read whole before anything is stored: the next tile may begin
+            uint32_t v[kChunks][32];
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int col = (2 * c + half) * 32;
+                if (col < BN && col < rows)
+                    tmem_ld_32x32b_x32_nowait(taddr + col, v[c]);
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+                tmem_ld_fence(v[c]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc * 8));
+            if (p.split > 1) {
+                // this pair's share of the sums, [row][128 outputs], over the finished stages
+                float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int col = (2 * c + half) * 32;
+                    if (BN <= 128 && col < BN && col < rows)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            sums[(col + k) * BM + quarter * 32 + lane] = __uint_as_float(v[c][k]);
+                }
+                continue;
+            }
+            const int j = at.j0 + static_cast<int>(cr) * BM + quarter * 32 + lane;
+            if (j >= p.d_out)
+                continue;
+            const float tw = p.tw == nullptr ? 1.f : __ldg(p.tw + at.e);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int col = (2 * c + half) * 32, count = rows - col;
+                if (col >= BN || count <= 0)
+                    continue;
+                const int64_t o = static_cast<int64_t>(at.b0 + col) * p.ldy + j;
+                if (p.yt == LNQ_BF16)
+                    store_column(static_cast<__nv_bfloat16 *>(p.y) + o, p.ldy, count, v[c], ta, tw);
+                else if (p.yt == LNQ_F16)
+                    store_column(static_cast<__half *>(p.y) + o, p.ldy, count, v[c], ta, tw);
+                else
+                    store_column(static_cast<float *>(p.y) + o, p.ldy, count, v[c], ta, tw);
+            }
+        }
+    }
+
+    if (p.split > 1) {
+        // One tile per cluster. Each pair adds and writes its share of the rows, over the pairs
+        // in order.
+        __syncwarp();
+        cluster_sync();
+        const Fp4TileAt at = tile_at<BN>(first, p, lim, pre);
+        const int rows = min(at.b1 - at.b0, BN);
+        const int r0 = part * rows / p.split, r1 = (part + 1) * rows / p.split;
+        const float ta = p.ta == nullptr ? 1.f : __ldg(p.ta);
+        const float tw = p.tw == nullptr ? 1.f : __ldg(p.tw + at.e);
+        uint32_t peer[kMaxSplit];
+#pragma unroll
+        for (int s = 0; s < kMaxSplit; ++s)
+            peer[s] = cluster_addr(smem, 2u * (s < p.split ? s : 0) + cr);
+        for (int i = r0 * BM + static_cast<int>(threadIdx.x); i < r1 * BM; i += kThreads) {
+            float sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < kMaxSplit; ++s)
+                if (s < p.split) {
+                    float u;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(peer[s] + i * 4));
+                    sum = s == 0 ? u : sum + u;
+                }
+            const int j = at.j0 + static_cast<int>(cr) * BM + i % BM;
+            if (j < p.d_out) {
+                const int64_t o = static_cast<int64_t>(at.b0 + i / BM) * p.ldy + j;
+                sum = sum * ta * tw;
+                if (p.yt == LNQ_BF16)
+                    static_cast<__nv_bfloat16 *>(p.y)[o] = from_f32<__nv_bfloat16>(sum);
+                else if (p.yt == LNQ_F16)
+                    static_cast<__half *>(p.y)[o] = from_f32<__half>(sum);
+                else
+                    static_cast<float *>(p.y)[o] = sum;
+            }
+        }
+    }
+
+    // All CTAs stay until the cluster is done: the MMAs read both CTAs' shared memory, barriers
+    // in the leader are signalled by both, partial sums are read by all.
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == kMmaWarp)
+        tmem_dealloc_pair(tmem_base, kTmemCols);
+}
+
+// ------------------------------------------------------------------------------------------
+// Host launcher
+// ------------------------------------------------------------------------------------------
+// Codes of `rows` rows as a byte matrix; boxes of 128 bytes x `box` rows.
+static bool encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t d, int box)
+{
+    auto encode = tensor_map_encoder();
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>((d + 1) / 2), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(fp4_code_pitch(d))};
+    cuuint32_t boxes[2] = {128, static_cast<cuuint32_t>(box)};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides,
+                  boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, int FMT>
+static cudaError_t gemm_tile(const Fp4Matrix &a, const Fp4Matrix &w, int64_t d_in, Fp4GemmParams p,
+                             int64_t tiles, int num_sms, cudaStream_t s)
+{
+    using T = f4::Tile<BN, FMT>;
+    CUtensorMap wmap, amap;
+    if (!encode_codes(&wmap, w.codes, p.w_total, d_in, f4::BM) ||
+        !encode_codes(&amap, a.codes, a.rows, d_in, BN / 2))
+        return cudaErrorInvalidValue;
+    auto kernel = fp4_gemm_kernel<BN, FMT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(T::kSmem));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * p.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(f4::kThreads);
+    cfg.dynamicSmemBytes = T::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.split == 1) {
+        static int resident = 0;  // pairs that run at once (one CTA per SM)
+        if (resident == 0) {
+            cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
+            int clusters = 0;
+            if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
+                (void)cudaGetLastError();  // a failed query is not an error of this call
+                clusters = num_sms / 2;
+            }
+            resident = clusters;
+        }
+        tiles = tiles < resident ? tiles : resident;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * 2 * p.split));
+    KernelTimer timer("lnq_fp4_gemm", s);
+    e = cudaLaunchKernelEx(&cfg, kernel, wmap, amap, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t fp4_gemm_launch(const Fp4Matrix &a, const int32_t *offsets, int64_t experts,
                             const Fp4Matrix &w, int64_t d_in, int fmt, void *y, int yt,
                             int64_t ldy, long long wait_limit, int num_sms, cudaStream_t s)
 {
-    (void)wait_limit, (void)num_sms;
-    const dim3 grid(static_cast<unsigned>((w.rows + kTile - 1) / kTile),
-                    static_cast<unsigned>(min((a.rows + kTile - 1) / kTile, int64_t(64))),
-                    static_cast<unsigned>(experts));
-    KernelTimer timer("lnq_fp4_gemm", s);
-    const bool mx = fmt == LNQ_FP4_MX;
-    switch (yt) {
-    case LNQ_F32:
-        (mx ? fp4_gemm_kernel<float, LNQ_FP4_MX> : fp4_gemm_kernel<float, LNQ_FP4_NV>)
-            <<<grid, 256, 0, s>>>(a, offsets, w, d_in, static_cast<float *>(y), ldy);
-        break;
-    case LNQ_BF16:
-        (mx ? fp4_gemm_kernel<__nv_bfloat16, LNQ_FP4_MX> : fp4_gemm_kernel<__nv_bfloat16, LNQ_FP4_NV>)
-            <<<grid, 256, 0, s>>>(a, offsets, w, d_in, static_cast<__nv_bfloat16 *>(y), ldy);
-        break;
-    case LNQ_F16:
-        (mx ? fp4_gemm_kernel<__half, LNQ_FP4_MX> : fp4_gemm_kernel<__half, LNQ_FP4_NV>)
-            <<<grid, 256, 0, s>>>(a, offsets, w, d_in, static_cast<__half *>(y), ldy);
-        break;
-    default: return cudaErrorInvalidValue;
+    if (tensor_map_encoder() == nullptr)
+        return cudaErrorNotSupported;
+    Fp4GemmParams p;
+    p.a_scales = a.scales;
+    p.w_scales = w.scales;
+    p.ta = a.t;
+    p.tw = w.t;
+    p.offsets = offsets;
+    p.y = y;
+    p.ldy = ldy;
+    p.w_total = w.rows * experts;
+    p.n = static_cast<int>(a.rows);
+    p.experts = static_cast<int>(experts);
+    p.d_out = static_cast<int>(w.rows);
+    p.yt = yt;
+    p.nk = static_cast<int>((d_in + f4::BK - 1) / f4::BK);
+    p.blocks = static_cast<int>((d_in + fp4_block(fmt) - 1) / fp4_block(fmt));
+    p.scale_pitch = static_cast<int>(fp4_scale_pitch(d_in, fmt));
+    p.mt = static_cast<int>((w.rows + f4::PM - 1) / f4::PM);
+    p.limit = wait_limit;
+    // rows per tile: the narrowest that holds a group of average size
+    const int64_t mean = (a.rows + experts - 1) / experts;
+    const int bn = mean <= 32 ? 32 : (mean <= 64 ? 64 : (mean <= 128 ? 128 : 256));
+    // an upper bound where the groups are not known here
+    const int64_t row_tiles = offsets == nullptr ? (a.rows + bn - 1) / bn
+                                                 : min(a.rows, a.rows / bn + experts);
+    const int64_t tiles = row_tiles * p.mt;
+    const int64_t pairs = num_sms / 2;
+    p.split = 1;
+    if (offsets == nullptr && bn <= 128)
+        while (p.split < f4::kMaxSplit && tiles * p.split * 2 <= pairs && p.nk >= p.split * 4)
+            p.split *= 2;
+    const bool nv = fmt == LNQ_FP4_NV;
+    switch (bn) {
+    case 32:
+        return nv ? gemm_tile<32, LNQ_FP4_NV>(a, w, d_in, p, tiles, num_sms, s)
+                  : gemm_tile<32, LNQ_FP4_MX>(a, w, d_in, p, tiles, num_sms, s);
+    case 64:
+        return nv ? gemm_tile<64, LNQ_FP4_NV>(a, w, d_in, p, tiles, num_sms, s)
+                  : gemm_tile<64, LNQ_FP4_MX>(a, w, d_in, p, tiles, num_sms, s);
+    case 128:
+        return nv ? gemm_tile<128, LNQ_FP4_NV>(a, w, d_in, p, tiles, num_sms, s)
+                  : gemm_tile<128, LNQ_FP4_MX>(a, w, d_in, p, tiles, num_sms, s);
+    default:
+        return nv ? gemm_tile<256, LNQ_FP4_NV>(a, w, d_in, p, tiles, num_sms, s)
+                  : gemm_tile<256, LNQ_FP4_MX>(a, w, d_in, p, tiles, num_sms, s);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t fp4_take_error_flags(uint32_t *flags, cudaStream_t s)
 {
-    const uint32_t zero[2] = {0u, 0u};
+    static const uint32_t zero[2] = {0u, 0u};
     cudaError_t e = cudaMemcpyFromSymbolAsync(flags, g_fp4_error, sizeof(uint32_t), 0,
                                               cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess)

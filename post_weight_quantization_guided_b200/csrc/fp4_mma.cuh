@@ -1,0 +1,100 @@
+// fp4_mma.cuh -- device helpers of the block-scaled 4-bit product: asynchronous scale copies, the
+// block-scaled pair MMA with its descriptors, and TMEM loads that are waited for together. Inline
+// PTX from the public PTX ISA for sm_100a.
+#pragma once
+
+#include "common.cuh"
+
+namespace lnq {
+
+// 4-byte asynchronous global -> shared copy of the first `bytes` (0..4) bytes, zeros behind them.
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst_smem, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst_smem),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Block-scaled product of a pair, kind::mxf4nvf4 (E2M1 operands, two 4-bit elements a byte, K = 64
+// per instruction): D (+)= (A sA) x (B sB) with the block scales read from both CTAs' TMEM.
+// kBlock16: four scales per row and instruction (blocks of 16), else two (blocks of 32).
+template <bool kBlock16>
+__device__ __forceinline__ void umma_f4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                             uint32_t accumulate)
+{
+    if constexpr (kBlock16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X"
+            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+            : "memory");
+}
+
+// 32 rows of 16 bytes of each CTA's shared memory (512 consecutive bytes) into four columns of its
+// TMEM, row i in lane i of all four lane quarters. Ordered before MMAs issued later by the thread.
+__device__ __forceinline__ void tmem_cp_32x128b_pair(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+// Shared-memory descriptor of 512 consecutive bytes (8-row groups of 128 bytes, no swizzle), the
+// source of tmem_cp_32x128b_pair.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t start)
+{
+    return static_cast<uint64_t>((start & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+           (static_cast<uint64_t>(1) << 46);
+}
+
+// Instruction descriptor for kind::mxf4nvf4: E2M1 operands, both K-major; power-of-two (E8M0) or
+// E4M3 scales; `sf` the byte of a scale word where the instruction's scales begin.
+__host__ __device__ constexpr uint32_t umma_idesc_f4(int M, int N, bool e8m0, uint32_t sf)
+{
+    return (sf << 4)                                  // B scales' byte
+           | (1u << 7) | (1u << 10)                   // A, B: E2M1
+           | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+           | ((e8m0 ? 1u : 0u) << 23)                 // scale type
+           | (static_cast<uint32_t>(M >> 4) << 24)    // M / 16 (a multiple of 8)
+           | (sf << 29);                              // A scales' byte
+}
+
+// 32 lanes x 32 columns of 32-bit values: thread t of the warp gets lane (base + t), columns
+// [col, col + 32). The registers may be read after tmem_ld_wait and tmem_ld_fence.
+__device__ __forceinline__ void tmem_ld_32x32b_x32_nowait(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Keeps the compiler from reading r before the wait that precedes this.
+__device__ __forceinline__ void tmem_ld_fence(uint32_t (&r)[32])
+{
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        asm volatile("" : "+r"(r[k]));
+}
+
+}  // namespace lnq
