@@ -10,14 +10,16 @@
 //
 // Per stage of 256 elements of K, a CTA's shared memory takes
 //   - both operands' codes by TMA (128 bytes a row, 128-byte swizzle), zeros outside the matrix;
-//   - the block scales of its 128 outputs and of all BN rows, row-major in memory, by 4-byte
-//     asynchronous copies that put row r's four scales of 64 (NV) or 128 (MX) elements where the
-//     tensor core wants them: byte 16 (r % 32) + 4 (r / 32 % 4) of a 512-byte atom per 128 rows.
+//   - the block scales of its 128 outputs and of all BN rows, row-major in memory, by 16- or 8-byte
+//     asynchronous copies; a warp then rearranges them in place: row r's four scales of 64 (NV) or
+//     128 (MX) elements go where the tensor core wants them, to byte 16 (r % 32) + 4 (r / 32 % 4)
+//     of a 512-byte atom per 128 rows. That warp has no loads of its own in flight, for which its
+//     proxy fence would wait.
 // The MMA thread copies the atoms to TMEM (tcgen05.cp, 4 columns each, a slot per stage so that no
-// copy overtakes an MMA that still reads) and issues four MMAs. All K-wise bounds are in the
-// copies: codes and scales behind the row's end arrive as zeros.
+// copy overtakes an MMA that still reads) and issues four MMAs. All K-wise bounds are in
+// these copies: codes and scales behind the row's end arrive as zeros.
 //
-// Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8-9 scales, 10 TMA,
+// Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8 loads, 9-10 scales,
 // 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs share the rows' tile.
 // With few tiles, `split` pairs of one cluster take a share of K each and add their sums through
 // distributed shared memory in a fixed order.
@@ -36,9 +38,8 @@ namespace f4 {
 constexpr int BM = 128, PM = 256;       // outputs of a CTA, of a pair
 constexpr int BK = 256;                 // elements of K per stage: 128 bytes of codes a row
 constexpr int kEpiWarps = 8, kScaleWarps = 2;  // 12 warps in all: 168 registers a thread
-constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kLoadWarp = kEpiWarps, kScaleWarp = kLoadWarp + 1, kMmaWarp = kScaleWarp + kScaleWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kScaleLag = 2;            // stages between a scale copy's issue and its hand-over
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSplit = 4;            // pairs of a cluster
 constexpr int kAtom = 512;              // bytes of scales of 128 rows x 4 blocks
@@ -54,12 +55,12 @@ struct Tile {
     static constexpr int kAcc = BN == 256 ? 1 : 2;                 // accumulators
     static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 7 : 8);
     static constexpr int kLimInts = LNQ_FP4_MAX_EXPERTS + 1;
-    static constexpr int kBars = 3 * kStages + 2 * kAcc + 1;
+    static constexpr int kBars = 4 * kStages + 2 * kAcc + 1;
     static constexpr size_t kSmem = static_cast<size_t>(kStages) * (kStageBytes + kScaleBytes) +
                                     2 * kLimInts * 4 + kBars * 8 + 32 + 1024 /* alignment */;
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(kStages * kSlotCols + kAcc * BN <= static_cast<int>(kTmemCols), "TMEM");
-    static_assert(kStageBytes % 1024 == 0 && kStages > kScaleLag, "stages");
+    static_assert(kStageBytes % 1024 == 0, "stages");
     static_assert(BN > 128 || BN * BM * 4 <= kStages * kStageBytes, "partial sums of a split");
 };
 }  // namespace f4
@@ -129,9 +130,10 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
     uint8_t *sf = smem + T::kStages * T::kStageBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sf + T::kStages * T::kScaleBytes);
-    uint64_t *full = bars;                           // codes landed (leader's: both CTAs')
-    uint64_t *scaled = full + T::kStages;            // scales landed (leader's: both CTAs')
-    uint64_t *empty = scaled + T::kStages;           // stage and TMEM slot free (each CTA's)
+    uint64_t *full = bars;                           // this CTA's codes have landed
+    uint64_t *raw = full + T::kStages;               // this CTA's scales have landed
+    uint64_t *ready = raw + T::kStages;              // leader's: both CTAs' stage may be multiplied
+    uint64_t *empty = ready + T::kStages;            // stage and TMEM slot free (each CTA's)
     uint64_t *tfull = empty + T::kStages;            // accumulator done (each CTA's)
     uint64_t *tempty = tfull + T::kAcc;              // accumulator read (leader's: both CTAs')
     uint64_t *drain = tempty + T::kAcc;
@@ -150,7 +152,8 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     if (threadIdx.x == 32) {
         for (int s = 0; s < T::kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&scaled[s], 2 * kScaleWarps);
+            mbar_init(&raw[s], 32);
+            mbar_init(&ready[s], 2);
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < T::kAcc; ++a) {
@@ -206,82 +209,37 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
     const int64_t num_tiles = static_cast<int64_t>(pre[p.experts]) * p.mt;
 
-    if (warp == kTmaWarp) {
-        // ------------------------------------------------------------------ codes by TMA
-        if (lane == 0) {
-            uint32_t fpar = 0u, fused = 0u;  // per stage: parity of the fills, ever filled
-            int stage = 0;
-            bool ok = true;
-            for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
-                const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
-                const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
-                const int arow = at.b0 + static_cast<int>(cr) * (BN / 2);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&empty[stage], ((fpar >> stage) & 1u) ^ 1u, p.limit)) {
-                        raise_error(err, kErrTimeout, 1);
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *st = smem + stage * T::kStageBytes;
-                    if (cr == 0)
-                        mbar_arrive_expect_tx(&full[stage], 2 * T::kStageBytes);
-                    const uint32_t fb = cluster_addr(&full[stage], leader);
-                    tma_load_2d_pair(st, &wmap, fb, kb * 128, wrow);
-                    tma_load_2d_pair(st + T::kABytes, &amap, fb, kb * 128, arow);
-                    fpar ^= 1u << stage;
-                    fused |= 1u << stage;
-                    stage = stage + 1 == T::kStages ? 0 : stage + 1;
-                }
-            }
-            if (!ok) {
-                // let this CTA's copies land: the leader waits for the last fill of each stage;
-                // its peer's copies are counted there, so the peer waits a fixed time
-                if (cr == 0) {
-                    for (int s = 0; s < T::kStages; ++s)
-                        if ((fused >> s) & 1u)
-                            mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, 1LL << 22);
-                } else {
-                    const long long c0 = clock64();
-                    while (clock64() - c0 < (1LL << 22)) {
-                    }
-                }
-            }
-        }
-    } else if (warp >= kEpiWarps && warp < kTmaWarp) {
-        // ------------------------------------------------------------------ block scales
-        constexpr int kSpan = kScaleWarps * 32;      // rows that the threads take at a time
-        constexpr int kSetsW = BM / kSpan, kSets = kSetsW + (BN + kSpan - 1) / kSpan;
-        const int r = threadIdx.x - kEpiWarps * 32;
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------------ loads
+        // Codes by TMA (lane 0), counted on `full`. Scales by asynchronous copies, a row's of the
+        // stage as one chunk of 4 W bytes at chunk 4 (i % 32) + i / 32 of its 128 rows, counted
+        // on `raw`. Nothing here waits for a load.
+        constexpr int W = T::kAtomsK;                 // words of scales per row and stage
+        constexpr int kGroups = 1 + T::kAtomsN;       // 128 outputs, then the tile's rows
+        const bool wide = p.scale_pitch % (4 * W) == 0 &&
+                          ((reinterpret_cast<uintptr_t>(p.w_scales) |
+                            reinterpret_cast<uintptr_t>(p.a_scales)) & (4 * W - 1)) == 0;
         const uint32_t sf_base = smem_u32(sf);
-        const uint32_t scaled_leader = cluster_addr(&scaled[0], leader);
-        uint32_t fpar = 0u;
-        int stage = 0, issued = 0, given = 0, given_stage = 0;
+        uint32_t fpar = 0u, fused = 0u;               // per stage: parity of the fills, ever filled
+        int stage = 0;
         bool ok = true;
-        auto hand_over = [&]() {  // this warp's copies of the oldest stage have landed
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(scaled_leader + static_cast<uint32_t>(given_stage * 8));
-            ++given;
-            given_stage = given_stage + 1 == T::kStages ? 0 : given_stage + 1;
-        };
         for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
             const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
-            // sets of rows: this CTA's outputs, then the tile's rows. Rows outside the arrays (and
-            // those whose sums nobody reads) get zeros.
-            const uint8_t *src[kSets];
-            int blocks[kSets];
+            const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
+            const int arow = at.b0 + static_cast<int>(cr) * (BN / 2);
+            // this lane's rows; rows outside the arrays (nobody reads their sums) go to row 0
+            const uint8_t *src[kGroups][4];
 #pragma unroll
-            for (int g = 0; g < kSets; ++g) {
-                const bool weights = g < kSetsW;
-                const int i = (weights ? g : g - kSetsW) * kSpan + r;
-                const int64_t row = weights ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
-                                                  static_cast<int>(cr) * BM + i
-                                            : static_cast<int64_t>(at.b0) + i;
-                const bool in = weights ? row < p.w_total : (i < BN && row < p.n);
-                src[g] = (weights ? p.w_scales : p.a_scales) + (in ? row : 0) * p.scale_pitch;
-                blocks[g] = in ? p.blocks : 0;
-            }
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int i = (lane >> 2) + 8 * m + 32 * (lane & 3);
+                    const int64_t row = g == 0 ? static_cast<int64_t>(wrow) + i
+                                               : static_cast<int64_t>(at.b0) + (g - 1) * 128 + i;
+                    const bool in = row < (g == 0 ? p.w_total : static_cast<int64_t>(p.n));
+                    src[g][m] = (g == 0 ? p.w_scales : p.a_scales) + (in ? row : 0) * p.scale_pitch;
+                }
+            const bool wanted = (lane & 3) * 32 < BN;  // of the rows' scales, for BN < 128
             for (int kb = kb0; kb < kb1; ++kb) {
                 int got = 0;
                 if (lane == 0)
@@ -289,39 +247,96 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 got = __shfl_sync(0xffffffffu, got, 0);
                 if (!got) {
                     if (lane == 0)
-                        raise_error(err, kErrTimeout, 2);
+                        raise_error(err, kErrTimeout, 1);
                     ok = false;
                     break;
                 }
-                const uint32_t dst = sf_base + static_cast<uint32_t>(stage * T::kScaleBytes);
+                if (lane == 0) {
+                    uint8_t *st = smem + stage * T::kStageBytes;
+                    mbar_arrive_expect_tx(&full[stage], T::kStageBytes);
+                    tma_load_2d(st, &wmap, &full[stage], kb * 128, wrow);
+                    tma_load_2d(st + T::kABytes, &amap, &full[stage], kb * 128, arow);
+                }
+                const int o = kb * 4 * W, bytes = min(p.blocks - o, 4 * W);
+                const uint32_t dst = sf_base + static_cast<uint32_t>(stage * T::kScaleBytes + lane * 4 * W);
 #pragma unroll
-                for (int g = 0; g < kSets; ++g) {
-                    const bool weights = g < kSetsW;
-                    const int i = (weights ? g : g - kSetsW) * kSpan + r;
-                    const uint32_t at_atom = static_cast<uint32_t>((i & 31) * 16 + ((i >> 5) & 3) * 4);
+                for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-                    for (int a = 0; a < T::kAtomsK; ++a) {
-                        const int k0 = (kb * T::kAtomsK + a) * 4;  // first block of the word
-                        const int atom = weights ? a : T::kAtomsK + a * T::kAtomsN + i / 128;
-                        const int bytes = min(max(blocks[g] - k0, 0), 4);
-                        if (weights || i < BN)
-                            cp_async4_zfill(dst + atom * kAtom + at_atom,
-                                            bytes > 0 ? src[g] + k0 : src[g],
-                                            static_cast<uint32_t>(bytes));
+                    for (int m = 0; m < 4; ++m) {
+                        if (g > 0 && !wanted)
+                            continue;
+                        const uint32_t to = dst + (g * 128 + m * 32) * 4 * W;
+                        if (wide) {
+                            cp_async_zfill<4 * W>(to, src[g][m] + o, bytes);
+                        } else {
+                            cp_async_zfill<2 * W>(to, src[g][m] + o, min(bytes, 2 * W));
+                            cp_async_zfill<2 * W>(to + 2 * W, src[g][m] + (bytes > 2 * W ? o + 2 * W : o),
+                                                  max(bytes - 2 * W, 0));
+                        }
                     }
-                }
-                cp_async_commit();
+                cp_async_arrive(&raw[stage]);
                 fpar ^= 1u << stage;
+                fused |= 1u << stage;
                 stage = stage + 1 == T::kStages ? 0 : stage + 1;
-                if (++issued > kScaleLag) {
-                    cp_async_wait_group<kScaleLag>();
-                    hand_over();
-                }
             }
         }
-        cp_async_wait_all();
-        while (given < issued)
-            hand_over();
+        if (!ok) {
+            // let this CTA's copies land before it exits
+            cp_async_wait_all();
+            if (lane == 0)
+                for (int s = 0; s < T::kStages; ++s)
+                    if ((fused >> s) & 1u)
+                        mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, kDrainLimit);
+        }
+    } else if (warp >= kScaleWarp && warp < kMmaWarp) {
+        // ------------------------------------------------------------------ scales into atoms
+        // 128 chunks of W words become W atoms of 128 words, in place. The warps take turns
+        // stage by stage; the one arrival on the leader also says that this CTA's codes are there.
+        constexpr int W = T::kAtomsK, kGroups = 1 + T::kAtomsN;
+        const uint32_t sf_base = smem_u32(sf);
+        const uint32_t ready_leader = cluster_addr(&ready[0], leader);
+        const int64_t tiles = first < num_tiles ? (num_tiles - first + step - 1) / step : 0;
+        const int64_t total = tiles * (kb1 - kb0);
+        int stage = warp - kScaleWarp;
+        uint32_t phase = 0u;
+        for (int64_t f = warp - kScaleWarp; f < total; f += kScaleWarps) {
+            int got = 0;
+            if (lane == 0)
+                got = mbar_wait(&raw[stage], phase, p.limit) && mbar_wait(&full[stage], phase, p.limit)
+                          ? 1 : 0;
+            got = __shfl_sync(0xffffffffu, got, 0);
+            if (!got) {
+                if (lane == 0)
+                    raise_error(err, kErrTimeout, 2);
+                break;
+            }
+            const uint32_t base = sf_base + static_cast<uint32_t>(stage * T::kScaleBytes);
+            uint32_t v[kGroups][4][W];
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    lds_words<W>(v[g][m], base + ((g * 4 + m) * 32 + lane) * 4 * W);
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int a = 0; a < W; ++a) {
+                        const int atom = g == 0 ? a : W + a * T::kAtomsN + g - 1;
+                        sts_word(base + atom * kAtom + (m * 32 + lane) * 4, v[g][m][a]);
+                    }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(ready_leader + static_cast<uint32_t>(stage * 8));
+            stage += kScaleWarps;
+            if (stage >= T::kStages) {
+                stage -= T::kStages;
+                phase ^= 1u;
+            }
+        }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------ MMA issue (leader)
         if (cr == 0 && lane == 0) {
@@ -339,8 +354,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&full[stage], (fph >> stage) & 1u, p.limit) ||
-                        !mbar_wait_cluster(&scaled[stage], (fph >> stage) & 1u, p.limit)) {
+                    if (!mbar_wait_cluster(&ready[stage], (fph >> stage) & 1u, p.limit)) {
                         raise_error(err, kErrTimeout, 4);
                         ok = false;
                         break;

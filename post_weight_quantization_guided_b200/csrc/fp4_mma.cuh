@@ -1,24 +1,50 @@
-// fp4_mma.cuh -- device helpers of the block-scaled 4-bit product: asynchronous scale copies, the
-// block-scaled pair MMA with its descriptors, and TMEM loads that are waited for together. Inline
-// PTX from the public PTX ISA for sm_100a.
+// fp4_mma.cuh -- device helpers of the block-scaled 4-bit product: the pair MMA with its
+// descriptors, the scales' copies, and TMEM loads that are waited for together. Inline PTX
+// from the public PTX ISA for sm_100a.
 #pragma once
 
 #include "common.cuh"
 
 namespace lnq {
 
-// 4-byte asynchronous global -> shared copy of the first `bytes` (0..4) bytes, zeros behind them.
-__device__ __forceinline__ void cp_async4_zfill(uint32_t dst_smem, const void *src, uint32_t bytes)
+// Asynchronous global -> shared copy of N (4, 8 or 16) bytes, of which the first `bytes` come from
+// src and the others are zeros.
+template <int N>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst_smem, const void *src, int bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst_smem),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem),
+                     "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst_smem),
+                     "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "n"(N)
+                     : "memory");
+}
+// An arrival on `bar` (counted among its expected ones) once this thread's copies so far are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group()
+
+// W (2 or 4) consecutive words of shared memory, one word.
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t (&v)[W], uint32_t addr)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    if constexpr (W == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void sts_word(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Block-scaled product of a pair, kind::mxf4nvf4 (E2M1 operands, two 4-bit elements a byte, K = 64
 // per instruction): D (+)= (A sA) x (B sB) with the block scales read from both CTAs' TMEM.
 // kBlock16: four scales per row and instruction (blocks of 16), else two (blocks of 32).
