@@ -8,19 +8,19 @@
 // rows (BN = 32 .. 256) with tcgen05.mma.cta_group::2.kind::mxf4nvf4 (M = 256, N = BN, K = 64 per
 // instruction); each CTA holds its 128 outputs' codes and half of the BN rows' codes.
 //
-// Per stage of 256 elements of K, a CTA's shared memory takes
-//   - both operands' codes by TMA (128 bytes a row, 128-byte swizzle), zeros outside the matrix;
-//   - the block scales of its 128 outputs and of all BN rows, row-major in memory, by 16- or 8-byte
-//     asynchronous copies; a warp then rearranges them in place: row r's four scales of 64 (NV) or
-//     128 (MX) elements go where the tensor core wants them, to byte 16 (r % 32) + 4 (r / 32 % 4)
-//     of a 512-byte atom per 128 rows. That warp has no loads of its own in flight, for which its
-//     proxy fence would wait.
-// The MMA thread copies the atoms to TMEM (tcgen05.cp, 4 columns each, a slot per stage so that no
-// copy overtakes an MMA that still reads) and issues four MMAs. All K-wise bounds are in
-// these copies: codes and scales behind the row's end arrive as zeros.
+// Codes come by TMA in stages of 256 elements of K (128 bytes a row, 128-byte swizzle, zeros
+// outside the matrix). The block scales of a CTA's 128 outputs and of all BN rows, row-major in
+// memory, come by asynchronous copies in steps of two stages, in a ring of their own; a warp
+// rearranges them in place: row r's four scales of 64 (NV) or 128 (MX) elements go where the
+// tensor core wants them, to byte 16 (r % 32) + 4 (r / 32 % 4) of a 512-byte atom per 128 rows.
+// (That warp has no loads of its own in flight, for which its proxy fence would wait.) The MMA
+// thread copies the atoms to TMEM (tcgen05.cp, 4 columns each, a slot per stage so that no copy
+// overtakes an MMA that still reads) and issues four MMAs a stage. All K-wise bounds are in these
+// copies: codes and scales behind the row's end arrive as zeros.
 //
-// Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8 loads, 9-10 scales,
-// 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs share the rows' tile.
+// Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8 codes, 9 scales,
+// 10 rearrangement, 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs
+// share the rows' tile.
 // With few tiles, `split` pairs of one cluster take a share of K each and add their sums through
 // distributed shared memory in a fixed order.
 #include <cstring>
@@ -37,9 +37,10 @@ __device__ uint32_t g_fp4_error[2];
 namespace f4 {
 constexpr int BM = 128, PM = 256;       // outputs of a CTA, of a pair
 constexpr int BK = 256;                 // elements of K per stage: 128 bytes of codes a row
-constexpr int kEpiWarps = 8, kScaleWarps = 2;  // 12 warps in all: 168 registers a thread
-constexpr int kLoadWarp = kEpiWarps, kScaleWarp = kLoadWarp + 1, kMmaWarp = kScaleWarp + kScaleWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kEpiWarps = 8;
+constexpr int kTmaWarp = 8, kLoadWarp = 9, kScaleWarp = 10, kMmaWarp = 11;
+constexpr int kThreads = 12 * 32;       // 168 registers a thread
+constexpr int kScaleRing = 4;           // steps (two stages each) of scales in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSplit = 4;            // pairs of a cluster
 constexpr int kAtom = 512;              // bytes of scales of 128 rows x 4 blocks
@@ -55,9 +56,9 @@ struct Tile {
     static constexpr int kAcc = BN == 256 ? 1 : 2;                 // accumulators
     static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 7 : 8);
     static constexpr int kLimInts = LNQ_FP4_MAX_EXPERTS + 1;
-    static constexpr int kBars = 4 * kStages + 2 * kAcc + 1;
-    static constexpr size_t kSmem = static_cast<size_t>(kStages) * (kStageBytes + kScaleBytes) +
-                                    2 * kLimInts * 4 + kBars * 8 + 32 + 1024 /* alignment */;
+    static constexpr int kBars = 2 * kStages + 3 * kScaleRing + 2 * kAcc + 1;
+    static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes +
+                                    2 * kScaleRing * kScaleBytes + 2 * kLimInts * 4 + kBars * 8 + 32 + 1024 /* alignment */;
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(kStages * kSlotCols + kAcc * BN <= static_cast<int>(kTmemCols), "TMEM");
     static_assert(kStageBytes % 1024 == 0, "stages");
@@ -129,12 +130,13 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
     uint8_t *sf = smem + T::kStages * T::kStageBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sf + T::kStages * T::kScaleBytes);
-    uint64_t *full = bars;                           // this CTA's codes have landed
-    uint64_t *raw = full + T::kStages;               // this CTA's scales have landed
-    uint64_t *ready = raw + T::kStages;              // leader's: both CTAs' stage may be multiplied
-    uint64_t *empty = ready + T::kStages;            // stage and TMEM slot free (each CTA's)
-    uint64_t *tfull = empty + T::kStages;            // accumulator done (each CTA's)
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sf + 2 * kScaleRing * T::kScaleBytes);
+    uint64_t *full = bars;                           // codes landed (leader's: both CTAs')
+    uint64_t *empty = full + T::kStages;             // stage and TMEM slot free (each CTA's)
+    uint64_t *sf_raw = empty + T::kStages;           // a step's scales landed (each CTA's)
+    uint64_t *sf_ready = sf_raw + kScaleRing;        // and are in place (leader's: both CTAs')
+    uint64_t *sf_empty = sf_ready + kScaleRing;      // and are in TMEM (each CTA's)
+    uint64_t *tfull = sf_empty + kScaleRing;         // accumulator done (each CTA's)
     uint64_t *tempty = tfull + T::kAcc;              // accumulator read (leader's: both CTAs')
     uint64_t *drain = tempty + T::kAcc;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
@@ -152,9 +154,12 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     if (threadIdx.x == 32) {
         for (int s = 0; s < T::kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&raw[s], 32);
-            mbar_init(&ready[s], 2);
             mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < kScaleRing; ++s) {
+            mbar_init(&sf_raw[s], 32);
+            mbar_init(&sf_ready[s], 2);
+            mbar_init(&sf_empty[s], 1);
         }
         for (int a = 0; a < T::kAcc; ++a) {
             mbar_init(&tfull[a], 1);
@@ -209,153 +214,187 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
     const int64_t num_tiles = static_cast<int64_t>(pre[p.experts]) * p.mt;
 
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------------------------ loads
-        // Codes by TMA (lane 0), counted on `full`. Scales by asynchronous copies, a row's of the
-        // stage as one chunk of 4 W bytes at chunk 4 (i % 32) + i / 32 of its 128 rows, counted
-        // on `raw`. Nothing here waits for a load.
+    if (warp == kTmaWarp) {
+        // ------------------------------------------------------------------ codes by TMA
+        if (lane == 0) {
+            uint32_t fpar = 0u, fused = 0u;  // per stage: parity of the fills, ever filled
+            int stage = 0;
+            bool ok = true;
+            for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+                const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
+                const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
+                const int arow = at.b0 + static_cast<int>(cr) * (BN / 2);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&empty[stage], ((fpar >> stage) & 1u) ^ 1u, p.limit)) {
+                        raise_error(err, kErrTimeout, 1);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = smem + stage * T::kStageBytes;
+                    if (cr == 0)
+                        mbar_arrive_expect_tx(&full[stage], 2 * T::kStageBytes);
+                    const uint32_t fb = cluster_addr(&full[stage], leader);
+                    tma_load_2d_pair(st, &wmap, fb, kb * 128, wrow);
+                    tma_load_2d_pair(st + T::kABytes, &amap, fb, kb * 128, arow);
+                    fpar ^= 1u << stage;
+                    fused |= 1u << stage;
+                    stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                }
+            }
+            if (!ok) {
+                // let this CTA's copies land: the leader waits for the last fill of each stage;
+                // its peer's copies are counted there, so the peer waits a fixed time
+                if (cr == 0) {
+                    for (int s = 0; s < T::kStages; ++s)
+                        if ((fused >> s) & 1u)
+                            mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, 1LL << 22);
+                } else {
+                    const long long c0 = clock64();
+                    while (clock64() - c0 < (1LL << 22)) {
+                    }
+                }
+            }
+        }
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------------------------ scales from memory
+        // A step is two stages: 8 W consecutive bytes of a row, two lanes' copies of 4 W bytes.
+        // The chunk of row i goes to place 4 (i % 32) + i / 32 of its 128 rows, so that a copy's
+        // 16 rows are consecutive chunks. Nothing here waits for a load.
         constexpr int W = T::kAtomsK;                 // words of scales per row and stage
         constexpr int kGroups = 1 + T::kAtomsN;       // 128 outputs, then the tile's rows
         const bool wide = p.scale_pitch % (4 * W) == 0 &&
                           ((reinterpret_cast<uintptr_t>(p.w_scales) |
                             reinterpret_cast<uintptr_t>(p.a_scales)) & (4 * W - 1)) == 0;
-        const uint32_t sf_base = smem_u32(sf);
-        uint32_t fpar = 0u, fused = 0u;               // per stage: parity of the fills, ever filled
-        int stage = 0;
+        const int half = lane & 1, quarter = (lane >> 1) & 3, i0 = (lane >> 3) + 32 * quarter;
+        const bool wanted = quarter * 32 < BN;        // of the rows' scales, for BN < 128
+        const uint32_t dst0 = smem_u32(sf) + static_cast<uint32_t>(half * T::kScaleBytes +
+                                                                   (lane >> 1) * 4 * W);
+        int slot = 0;
+        uint32_t phase = 1u;
         bool ok = true;
         for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
             const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
-            const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
-            const int arow = at.b0 + static_cast<int>(cr) * (BN / 2);
-            // this lane's rows; rows outside the arrays (nobody reads their sums) go to row 0
-            const uint8_t *src[kGroups][4];
+            // rows outside the arrays (nobody reads their sums) repeat the last one
+            const uint8_t *src[kGroups][8];
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
+            for (int g = 0; g < kGroups; ++g) {
+                const int64_t r0 = i0 + (g == 0 ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
+                                                      static_cast<int>(cr) * BM
+                                                : static_cast<int64_t>(at.b0) + (g - 1) * 128);
+                const int64_t top = (g == 0 ? p.w_total : static_cast<int64_t>(p.n)) - 1;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int i = (lane >> 2) + 8 * m + 32 * (lane & 3);
-                    const int64_t row = g == 0 ? static_cast<int64_t>(wrow) + i
-                                               : static_cast<int64_t>(at.b0) + (g - 1) * 128 + i;
-                    const bool in = row < (g == 0 ? p.w_total : static_cast<int64_t>(p.n));
-                    src[g][m] = (g == 0 ? p.w_scales : p.a_scales) + (in ? row : 0) * p.scale_pitch;
-                }
-            const bool wanted = (lane & 3) * 32 < BN;  // of the rows' scales, for BN < 128
-            for (int kb = kb0; kb < kb1; ++kb) {
+                for (int m = 0; m < 8; ++m)
+                    src[g][m] = (g == 0 ? p.w_scales : p.a_scales) + min(r0 + 4 * m, top) * p.scale_pitch;
+            }
+            for (int kb = kb0; kb < kb1; kb += 2) {
                 int got = 0;
                 if (lane == 0)
-                    got = mbar_wait(&empty[stage], ((fpar >> stage) & 1u) ^ 1u, p.limit) ? 1 : 0;
+                    got = mbar_wait(&sf_empty[slot], phase, p.limit) ? 1 : 0;
                 got = __shfl_sync(0xffffffffu, got, 0);
                 if (!got) {
                     if (lane == 0)
-                        raise_error(err, kErrTimeout, 1);
+                        raise_error(err, kErrTimeout, 2);
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
-                    uint8_t *st = smem + stage * T::kStageBytes;
-                    mbar_arrive_expect_tx(&full[stage], T::kStageBytes);
-                    tma_load_2d(st, &wmap, &full[stage], kb * 128, wrow);
-                    tma_load_2d(st + T::kABytes, &amap, &full[stage], kb * 128, arow);
-                }
-                const int o = kb * 4 * W, bytes = min(p.blocks - o, 4 * W);
-                const uint32_t dst = sf_base + static_cast<uint32_t>(stage * T::kScaleBytes + lane * 4 * W);
+                const int o = (kb + half) * 4 * W, bytes = min(max(p.blocks - o, 0), 4 * W);
+                const int from = bytes > 0 ? o : 0;
+                const uint32_t dst = dst0 + static_cast<uint32_t>(slot * 2 * T::kScaleBytes);
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g)
+                for (int g = 0; g < kGroups; ++g) {
+                    if (g > 0 && !wanted)
+                        continue;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        if (g > 0 && !wanted)
-                            continue;
-                        const uint32_t to = dst + (g * 128 + m * 32) * 4 * W;
+                    for (int m = 0; m < 8; ++m) {
+                        const uint32_t to = dst + (g * 128 + m * 16) * 4 * W;
                         if (wide) {
-                            cp_async_zfill<4 * W>(to, src[g][m] + o, bytes);
+                            cp_async_zfill<4 * W>(to, src[g][m] + from, bytes);
                         } else {
-                            cp_async_zfill<2 * W>(to, src[g][m] + o, min(bytes, 2 * W));
-                            cp_async_zfill<2 * W>(to + 2 * W, src[g][m] + (bytes > 2 * W ? o + 2 * W : o),
+                            cp_async_zfill<2 * W>(to, src[g][m] + from, min(bytes, 2 * W));
+                            cp_async_zfill<2 * W>(to + 2 * W, src[g][m] + from + (bytes > 2 * W ? 2 * W : 0),
                                                   max(bytes - 2 * W, 0));
                         }
                     }
-                cp_async_arrive(&raw[stage]);
-                fpar ^= 1u << stage;
-                fused |= 1u << stage;
-                stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                }
+                cp_async_arrive(&sf_raw[slot]);
+                slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                phase ^= slot == 0 ? 1u : 0u;
             }
         }
-        if (!ok) {
-            // let this CTA's copies land before it exits
-            cp_async_wait_all();
-            if (lane == 0)
-                for (int s = 0; s < T::kStages; ++s)
-                    if ((fused >> s) & 1u)
-                        mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, kDrainLimit);
-        }
-    } else if (warp >= kScaleWarp && warp < kMmaWarp) {
+        cp_async_wait_all();  // this CTA's copies have landed before it exits
+    } else if (warp == kScaleWarp) {
         // ------------------------------------------------------------------ scales into atoms
-        // 128 chunks of W words become W atoms of 128 words, in place. The warps take turns
-        // stage by stage; the one arrival on the leader also says that this CTA's codes are there.
+        // 128 chunks of W words become W atoms of 128 words, in place.
         constexpr int W = T::kAtomsK, kGroups = 1 + T::kAtomsN;
-        const uint32_t sf_base = smem_u32(sf);
-        const uint32_t ready_leader = cluster_addr(&ready[0], leader);
-        const int64_t tiles = first < num_tiles ? (num_tiles - first + step - 1) / step : 0;
-        const int64_t total = tiles * (kb1 - kb0);
-        int stage = warp - kScaleWarp;
+        const uint32_t ready_leader = cluster_addr(&sf_ready[0], leader);
+        int slot = 0;
         uint32_t phase = 0u;
-        for (int64_t f = warp - kScaleWarp; f < total; f += kScaleWarps) {
-            int got = 0;
-            if (lane == 0)
-                got = mbar_wait(&raw[stage], phase, p.limit) && mbar_wait(&full[stage], phase, p.limit)
-                          ? 1 : 0;
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got) {
+        bool ok = true;
+        for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+            for (int kb = kb0; kb < kb1; kb += 2) {
+                int got = 0;
                 if (lane == 0)
-                    raise_error(err, kErrTimeout, 2);
-                break;
-            }
-            const uint32_t base = sf_base + static_cast<uint32_t>(stage * T::kScaleBytes);
-            uint32_t v[kGroups][4][W];
+                    got = mbar_wait(&sf_raw[slot], phase, p.limit) ? 1 : 0;
+                got = __shfl_sync(0xffffffffu, got, 0);
+                if (!got) {
+                    if (lane == 0)
+                        raise_error(err, kErrTimeout, 3);
+                    ok = false;
+                    break;
+                }
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t base = smem_u32(sf) +
+                                          static_cast<uint32_t>((slot * 2 + h) * T::kScaleBytes);
+                    uint32_t v[kGroups][4][W];
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    lds_words<W>(v[g][m], base + ((g * 4 + m) * 32 + lane) * 4 * W);
-            __syncwarp();
+                    for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
+                        for (int m = 0; m < 4; ++m)
+                            lds_words<W>(v[g][m], base + ((g * 4 + m) * 32 + lane) * 4 * W);
+                    __syncwarp();
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
+                    for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-                    for (int a = 0; a < W; ++a) {
-                        const int atom = g == 0 ? a : W + a * T::kAtomsN + g - 1;
-                        sts_word(base + atom * kAtom + (m * 32 + lane) * 4, v[g][m][a]);
-                    }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(ready_leader + static_cast<uint32_t>(stage * 8));
-            stage += kScaleWarps;
-            if (stage >= T::kStages) {
-                stage -= T::kStages;
-                phase ^= 1u;
+                        for (int m = 0; m < 4; ++m)
+#pragma unroll
+                            for (int a = 0; a < W; ++a) {
+                                const int atom = g == 0 ? a : W + a * T::kAtomsN + g - 1;
+                                sts_word(base + atom * kAtom + (m * 32 + lane) * 4, v[g][m][a]);
+                            }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(ready_leader + static_cast<uint32_t>(slot * 8));
+                slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                phase ^= slot == 0 ? 1u : 0u;
             }
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------ MMA issue (leader)
-        if (cr == 0 && lane == 0) {
+        // The whole warp waits, one elected lane issues (always the same one: the warp stays
+        // converged), so that operands stay in uniform registers.
+        if (cr == 0) {
             constexpr bool kNv = FMT == LNQ_FP4_NV;
-            int stage = 0, it = 0;
-            uint32_t fph = 0u;  // per stage: phase parity
+            int stage = 0, it = 0, sslot = 0;
+            uint32_t fph = 0u, sphase = 0u;  // phase parities
             bool ok = true;
             for (int64_t tile = first; tile < num_tiles && ok; tile += step, ++it) {
                 const int acc = it % T::kAcc, use = it / T::kAcc;
-                if (!mbar_wait_cluster(&tempty[acc], (use & 1) ^ 1, p.limit)) {
-                    raise_error(err, kErrTimeout, 3);
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], (use & 1) ^ 1, p.limit))) {
+                    raise_error(err, kErrTimeout, 4);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait_cluster(&ready[stage], (fph >> stage) & 1u, p.limit)) {
-                        raise_error(err, kErrTimeout, 4);
+                    const int h = (kb - kb0) & 1;  // stage of the step
+                    if (!__all_sync(0xffffffffu,
+                                    (h == 1 || mbar_wait_cluster(&sf_ready[sslot], sphase, p.limit)) &&
+                                        mbar_wait(&full[stage], (fph >> stage) & 1u, p.limit))) {
+                        raise_error(err, kErrTimeout, 5);
                         ok = false;
                         break;
                     }
@@ -363,31 +402,44 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * T::kStageBytes);
                     const uint32_t sb = sa + T::kABytes;
-                    const uint32_t ss = smem_u32(sf + stage * T::kScaleBytes);
+                    const uint32_t ss = smem_u32(sf + (sslot * 2 + h) * T::kScaleBytes);
                     const uint32_t slot =
                         tmem_base + static_cast<uint32_t>(T::kAcc * BN + stage * T::kSlotCols);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int c = 0; c < T::kAtomsK * (1 + T::kAtomsN); ++c)
-                        tmem_cp_32x128b_pair(slot + c * 4, smem_desc_plain(ss + c * kAtom));
+                        for (int c = 0; c < T::kAtomsK * (1 + T::kAtomsN); ++c)
+                            tmem_cp_32x128b_pair(slot + c * 4, smem_desc_plain(ss + c * kAtom));
 #pragma unroll
-                    for (int kk = 0; kk < BK / 64; ++kk) {
-                        const int atom = kNv ? kk : kk / 2;
-                        const uint32_t idesc = umma_idesc_f4(PM, BN, !kNv, kNv ? 0u : (kk & 1) * 2u);
-                        const uint64_t ad = umma_desc_sw128(sa + kk * 32, 16, 1024);
-                        const uint64_t bd = umma_desc_sw128(sb + kk * 32, 16, 1024);
-                        umma_f4_pair<kNv>(d_tmem, ad, bd, idesc, slot + atom * 4,
-                                          slot + (T::kAtomsK + atom * T::kAtomsN) * 4,
-                                          (kb != kb0 || kk != 0) ? 1u : 0u);
+                        for (int kk = 0; kk < BK / 64; ++kk) {
+                            const int atom = kNv ? kk : kk / 2;
+                            const uint32_t idesc = umma_idesc_f4(PM, BN, !kNv, kNv ? 0u : (kk & 1) * 2u);
+                            const uint64_t ad = umma_desc_sw128(sa + kk * 32, 16, 1024);
+                            const uint64_t bd = umma_desc_sw128(sb + kk * 32, 16, 1024);
+                            umma_f4_pair<kNv>(d_tmem, ad, bd, idesc, slot + atom * 4,
+                                              slot + (T::kAtomsK + atom * T::kAtomsN) * 4,
+                                              (kb != kb0 || kk != 0) ? 1u : 0u);
+                        }
+                        umma_commit_pair(&empty[stage], pair_mask);
+                        if (h == 1 || kb + 1 == kb1)
+                            umma_commit_pair(&sf_empty[sslot], pair_mask);
                     }
-                    umma_commit_pair(&empty[stage], pair_mask);
+                    __syncwarp();
+                    if (h == 1 || kb + 1 == kb1) {
+                        sslot = sslot + 1 == kScaleRing ? 0 : sslot + 1;
+                        sphase ^= sslot == 0 ? 1u : 0u;
+                    }
                     stage = stage + 1 == T::kStages ? 0 : stage + 1;
                 }
                 if (!ok)
                     break;
-                umma_commit_pair(&tfull[acc], pair_mask);
+                if (elect_one())
+                    umma_commit_pair(&tfull[acc], pair_mask);
+                __syncwarp();
             }
-            // every MMA of this thread has completed once `drain` flips
-            umma_commit_pair(drain, static_cast<uint16_t>(1u << leader));
+            // every MMA of this warp has completed once `drain` flips
+            if (elect_one())
+                umma_commit_pair(drain, static_cast<uint16_t>(1u << leader));
+            __syncwarp();
             mbar_wait(drain, 0, kDrainLimit);
         }
     } else {
@@ -405,7 +457,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) {
                 if (lane == 0)
-                    raise_error(err, kErrTimeout, 5);
+                    raise_error(err, kErrTimeout, 6);
                 break;
             }
             __syncwarp();

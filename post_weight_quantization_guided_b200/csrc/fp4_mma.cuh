@@ -28,6 +28,14 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
                  : "memory");
 }
 
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0u;
+}
+
 // W (2 or 4) consecutive words of shared memory, one word.
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t (&v)[W], uint32_t addr)
