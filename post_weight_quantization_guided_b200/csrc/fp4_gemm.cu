@@ -9,14 +9,15 @@
 // instruction); each CTA holds its 128 outputs' codes and half of the BN rows' codes.
 //
 // Codes come by TMA in stages of 256 elements of K (128 bytes a row, 128-byte swizzle, zeros
-// outside the matrix). The block scales of a CTA's 128 outputs and of all BN rows, row-major in
-// memory, come by asynchronous copies in steps of two stages, in a ring of their own; a warp
-// rearranges them in place: row r's four scales of 64 (NV) or 128 (MX) elements go where the
-// tensor core wants them, to byte 16 (r % 32) + 4 (r / 32 % 4) of a 512-byte atom per 128 rows.
-// (That warp has no loads of its own in flight, for which its proxy fence would wait.) The MMA
-// thread copies the atoms to TMEM (tcgen05.cp, 4 columns each, a slot per stage so that no copy
-// overtakes an MMA that still reads) and issues four MMAs a stage. All K-wise bounds are in these
-// copies: codes and scales behind the row's end arrive as zeros.
+// outside the matrix), the block scales of a CTA's 128 outputs and of all BN rows by TMA in steps
+// of two stages, in a ring of their own. A warp rearranges the scales in place: row r's four scales
+// of 64 (NV) or 128 (MX) elements go where the tensor core wants them, to byte 16 (r % 32) +
+// 4 (r / 32 % 4) of a 512-byte atom per 128 rows. (Nothing but TMA may be in flight for the proxy
+// fence that follows: it waits for asynchronous copies of the CTA's other warps and for loads of its
+// own, which cost 1.2 us a step.) The MMA thread copies the atoms to TMEM (tcgen05.cp, 4 columns
+// each, a slot per stage so that no copy overtakes an MMA that still reads) and issues four MMAs
+// a stage. All K-wise bounds are in these copies: codes and scales behind the row's end arrive as
+// zeros.
 //
 // Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8 codes, 9 scales,
 // 10 rearrangement, 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs
@@ -51,6 +52,14 @@ struct Tile {
     static constexpr int kAtomsN = (BN + 127) / 128;              // along the rows
     static constexpr int kABytes = BM * 128, kBBytes = BN / 2 * 128;
     static constexpr int kScaleBytes = kAtomsK * (1 + kAtomsN) * kAtom;
+    static constexpr int kRowBytes = 8 * kAtomsK;                  // scales of a row and step
+    static constexpr int kStepBytes = 2 * kScaleBytes;
+    // Offset of 16-byte chunk c of row i of a step's scales as they come (see the load warp).
+    static __device__ __forceinline__ uint32_t chunk_at(int i, int c)
+    {
+        return kRowBytes == 32 ? static_cast<uint32_t>(i * 32 + ((c ^ (i >> 2)) & 1) * 16)
+                               : static_cast<uint32_t>(i * 16);
+    }
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kSlotCols = kAtomsK * 4 * (1 + kAtomsN);  // TMEM columns of a stage's scales
     static constexpr int kAcc = BN == 256 ? 1 : 2;                 // accumulators
@@ -58,7 +67,7 @@ struct Tile {
     static constexpr int kLimInts = LNQ_FP4_MAX_EXPERTS + 1;
     static constexpr int kBars = 2 * kStages + 3 * kScaleRing + 2 * kAcc + 1;
     static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes +
-                                    2 * kScaleRing * kScaleBytes + 2 * kLimInts * 4 + kBars * 8 + 32 + 1024 /* alignment */;
+                                    kScaleRing * kStepBytes + 2 * kLimInts * 4 + kBars * 8 + 32 + 1024 /* alignment */;
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(kStages * kSlotCols + kAcc * BN <= static_cast<int>(kTmemCols), "TMEM");
     static_assert(kStageBytes % 1024 == 0, "stages");
@@ -80,6 +89,7 @@ struct Fp4GemmParams {
     int scale_pitch;       // bytes
     int mt;                // output tiles of one matrix
     int split;             // pairs that share a tile's K
+    int sf_tma;            // scales by TMA: rows are multiples of 16 bytes
     long long limit;
 };
 
@@ -123,14 +133,18 @@ __device__ __forceinline__ Fp4TileAt tile_at(int64_t tile, const Fp4GemmParams &
 template <int BN, int FMT>
 __global__ void __launch_bounds__(f4::kThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
-                    const __grid_constant__ CUtensorMap amap, const Fp4GemmParams p)
+                    const __grid_constant__ CUtensorMap amap,
+                    const __grid_constant__ CUtensorMap wsmap,
+                    const __grid_constant__ CUtensorMap asmap, const Fp4GemmParams p)
 {
     using namespace f4;
     using T = Tile<BN, FMT>;
+    constexpr int W = T::kAtomsK;            // words of scales per row and stage
+    constexpr int kGroups = 1 + T::kAtomsN;  // of 128 rows of scales: outputs, then the tile's rows
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
     uint8_t *sf = smem + T::kStages * T::kStageBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sf + 2 * kScaleRing * T::kScaleBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sf + kScaleRing * T::kStepBytes);
     uint64_t *full = bars;                           // codes landed (leader's: both CTAs')
     uint64_t *empty = full + T::kStages;             // stage and TMEM slot free (each CTA's)
     uint64_t *sf_raw = empty + T::kStages;           // a step's scales landed (each CTA's)
@@ -148,7 +162,9 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     const int part = static_cast<int>(rank >> 1);          // this pair's share of K
     const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
     const int64_t first = blockIdx.x / (2 * p.split), step = gridDim.x / (2 * p.split);
-    const int kb0 = part * p.nk / p.split, kb1 = (part + 1) * p.nk / p.split;
+    const int steps = (p.nk + 1) / 2;  // of two stages
+    const int kb0 = part * steps / p.split * 2;
+    const int kb1 = min((part + 1) * steps / p.split * 2, p.nk);
     DeviceErr err{g_fp4_error, p.limit};
 
     if (threadIdx.x == 32) {
@@ -157,7 +173,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < kScaleRing; ++s) {
-            mbar_init(&sf_raw[s], 32);
+            mbar_init(&sf_raw[s], p.sf_tma ? 1 : 32);
             mbar_init(&sf_ready[s], 2);
             mbar_init(&sf_empty[s], 1);
         }
@@ -169,6 +185,10 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
         fence_barrier_init();
         tma_prefetch_desc(&wmap);
         tma_prefetch_desc(&amap);
+        if (p.sf_tma) {
+            tma_prefetch_desc(&wsmap);
+            tma_prefetch_desc(&asmap);
+        }
     }
     if (warp == kMmaWarp)
         tmem_alloc_pair(tmem_holder, kTmemCols);
@@ -257,112 +277,141 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------------ scales from memory
-        // A step is two stages: 8 W consecutive bytes of a row, two lanes' copies of 4 W bytes.
-        // The chunk of row i goes to place 4 (i % 32) + i / 32 of its 128 rows, so that a copy's
-        // 16 rows are consecutive chunks. Nothing here waits for a load.
-        constexpr int W = T::kAtomsK;                 // words of scales per row and stage
-        constexpr int kGroups = 1 + T::kAtomsN;       // 128 outputs, then the tile's rows
-        const bool wide = p.scale_pitch % (4 * W) == 0 &&
-                          ((reinterpret_cast<uintptr_t>(p.w_scales) |
-                            reinterpret_cast<uintptr_t>(p.a_scales)) & (4 * W - 1)) == 0;
-        const int half = lane & 1, quarter = (lane >> 1) & 3, i0 = (lane >> 3) + 32 * quarter;
-        const bool wanted = quarter * 32 < BN;        // of the rows' scales, for BN < 128
-        const uint32_t dst0 = smem_u32(sf) + static_cast<uint32_t>(half * T::kScaleBytes +
-                                                                   (lane >> 1) * 4 * W);
-        int slot = 0;
-        uint32_t phase = 1u;
-        bool ok = true;
-        for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
-            const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
-            // rows outside the arrays (nobody reads their sums) repeat the last one
-            const uint8_t *src[kGroups][8];
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int64_t r0 = i0 + (g == 0 ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
-                                                      static_cast<int>(cr) * BM
-                                                : static_cast<int64_t>(at.b0) + (g - 1) * 128);
-                const int64_t top = (g == 0 ? p.w_total : static_cast<int64_t>(p.n)) - 1;
-#pragma unroll
-                for (int m = 0; m < 8; ++m)
-                    src[g][m] = (g == 0 ? p.w_scales : p.a_scales) + min(r0 + 4 * m, top) * p.scale_pitch;
-            }
-            for (int kb = kb0; kb < kb1; kb += 2) {
-                int got = 0;
-                if (lane == 0)
-                    got = mbar_wait(&sf_empty[slot], phase, p.limit) ? 1 : 0;
-                got = __shfl_sync(0xffffffffu, got, 0);
-                if (!got) {
-                    if (lane == 0)
-                        raise_error(err, kErrTimeout, 2);
-                    ok = false;
-                    break;
-                }
-                const int o = (kb + half) * 4 * W, bytes = min(max(p.blocks - o, 0), 4 * W);
-                const int from = bytes > 0 ? o : 0;
-                const uint32_t dst = dst0 + static_cast<uint32_t>(slot * 2 * T::kScaleBytes);
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    if (g > 0 && !wanted)
-                        continue;
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        const uint32_t to = dst + (g * 128 + m * 16) * 4 * W;
-                        if (wide) {
-                            cp_async_zfill<4 * W>(to, src[g][m] + from, bytes);
-                        } else {
-                            cp_async_zfill<2 * W>(to, src[g][m] + from, min(bytes, 2 * W));
-                            cp_async_zfill<2 * W>(to + 2 * W, src[g][m] + from + (bytes > 2 * W ? 2 * W : 0),
-                                                  max(bytes - 2 * W, 0));
+        // A step is two stages: 8 W bytes of a row, 32 (NV, their 16-byte halves exchanged in
+        // every second four rows: TMA's 32-byte swizzle) or 16 (MX) bytes of shared memory a row.
+        if (p.sf_tma) {
+            if (lane == 0) {
+                int slot = 0;
+                uint32_t phase = 1u, fused = 0u;
+                bool ok = true;
+                for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+                    const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
+                    const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
+                    for (int kb = kb0; kb < kb1; kb += 2) {
+                        if (!mbar_wait(&sf_empty[slot], phase, p.limit)) {
+                            raise_error(err, kErrTimeout, 2);
+                            ok = false;
+                            break;
                         }
+                        uint8_t *st = sf + slot * T::kStepBytes;
+                        mbar_arrive_expect_tx(&sf_raw[slot], (BM + BN) * T::kRowBytes);
+                        tma_load_2d(st, &wsmap, &sf_raw[slot], kb * 4 * W, wrow);
+                        tma_load_2d(st + BM * T::kRowBytes, &asmap, &sf_raw[slot], kb * 4 * W, at.b0);
+                        fused |= 1u << slot;
+                        slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                        phase ^= slot == 0 ? 1u : 0u;
                     }
                 }
-                cp_async_arrive(&sf_raw[slot]);
-                slot = slot + 1 == kScaleRing ? 0 : slot + 1;
-                phase ^= slot == 0 ? 1u : 0u;
+                if (!ok)  // let the copies land before this CTA exits
+                    for (int s = 0; s < kScaleRing; ++s)
+                        if ((fused >> s) & 1u)
+                            mbar_wait(&sf_raw[s], s < slot ? phase ^ 1u : phase, kDrainLimit);
+            }
+        } else {
+            // Rows that are no multiples of 16 bytes: loads of half a stage's bytes, one step
+            // ahead of their stores, in registers.
+            uint32_t v[kGroups * 4][2 * W];
+            int64_t next_tile = first;
+            int next_kb = kb0;
+            Fp4TileAt at = {0, 0, 0, 0};
+            if (next_tile < num_tiles)
+                at = tile_at<BN>(next_tile, p, lim, pre);
+            auto fetch = [&]() {
+                if (next_tile >= num_tiles)
+                    return;
+#pragma unroll
+                for (int g = 0; g < kGroups * 4; ++g) {
+                    // rows outside the arrays (nobody reads their sums) repeat the last one
+                    const int64_t row = g < 4 ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
+                                                    static_cast<int>(cr) * BM + g * 32 + lane
+                                              : static_cast<int64_t>(at.b0) + (g - 4) * 32 + lane;
+                    const int64_t top = (g < 4 ? p.w_total : static_cast<int64_t>(p.n)) - 1;
+                    const uint8_t *src = (g < 4 ? p.w_scales : p.a_scales) + min(row, top) * p.scale_pitch;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int o = next_kb * 4 * W + u * 2 * W;
+#pragma unroll
+                        for (int k = 0; k < W / 2; ++k)
+                            v[g][u * (W / 2) + k] = 0u;
+                        if (o < p.scale_pitch && (g - 4) * 32 < BN)
+                            ldg_words<W / 2>(v[g] + u * (W / 2), src + o);
+                    }
+                }
+                next_kb += 2;
+                if (next_kb >= kb1) {
+                    next_kb = kb0;
+                    next_tile += step;
+                    if (next_tile < num_tiles)
+                        at = tile_at<BN>(next_tile, p, lim, pre);
+                }
+            };
+            fetch();
+            int slot = 0;
+            uint32_t phase = 1u;
+            bool ok = true;
+            for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+                for (int kb = kb0; kb < kb1; kb += 2) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase, p.limit))) {
+                        if (lane == 0)
+                            raise_error(err, kErrTimeout, 2);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
+#pragma unroll
+                    for (int g = 0; g < kGroups * 4; ++g) {
+                        if ((g - 4) * 32 >= BN)
+                            continue;
+                        uint32_t *w = v[g];
+#pragma unroll
+                        for (int k = 0; k < 2 * W; ++k)  // nothing behind the row's last block
+                            w[k] &= first_bytes(p.blocks - kb * 4 * W - 4 * k);
+#pragma unroll
+                        for (int c = 0; c < W / 2; ++c)
+                            sts_words4(st + T::chunk_at(g * 32 + lane, c), w[4 * c], w[4 * c + 1],
+                                       w[4 * c + 2], w[4 * c + 3]);
+                    }
+                    mbar_arrive(&sf_raw[slot]);
+                    fetch();
+                    slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                    phase ^= slot == 0 ? 1u : 0u;
+                }
             }
         }
-        cp_async_wait_all();  // this CTA's copies have landed before it exits
     } else if (warp == kScaleWarp) {
         // ------------------------------------------------------------------ scales into atoms
-        // 128 chunks of W words become W atoms of 128 words, in place.
-        constexpr int W = T::kAtomsK, kGroups = 1 + T::kAtomsN;
+        // Lane l takes rows l, l + 32, l + 64, l + 96 of each 128 and writes, for each word of
+        // the rows, the four rows' words as 16 bytes of the word's atom: in place, so everything is
+        // read before anything is written.
         const uint32_t ready_leader = cluster_addr(&sf_ready[0], leader);
         int slot = 0;
         uint32_t phase = 0u;
         bool ok = true;
         for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
             for (int kb = kb0; kb < kb1; kb += 2) {
-                int got = 0;
-                if (lane == 0)
-                    got = mbar_wait(&sf_raw[slot], phase, p.limit) ? 1 : 0;
-                got = __shfl_sync(0xffffffffu, got, 0);
-                if (!got) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&sf_raw[slot], phase, p.limit))) {
                     if (lane == 0)
                         raise_error(err, kErrTimeout, 3);
                     ok = false;
                     break;
                 }
+                const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
+                uint32_t v[kGroups * 4][2 * W];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t base = smem_u32(sf) +
-                                          static_cast<uint32_t>((slot * 2 + h) * T::kScaleBytes);
-                    uint32_t v[kGroups][4][W];
+                for (int g = 0; g < kGroups * 4; ++g)
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
+                    for (int c = 0; c < W / 2; ++c)
+                        lds_words4(v[g] + 4 * c, st + T::chunk_at(g * 32 + lane, c));
+                __syncwarp();
 #pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            lds_words<W>(v[g][m], base + ((g * 4 + m) * 32 + lane) * 4 * W);
-                    __syncwarp();
+                for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-#pragma unroll
-                            for (int a = 0; a < W; ++a) {
-                                const int atom = g == 0 ? a : W + a * T::kAtomsN + g - 1;
-                                sts_word(base + atom * kAtom + (m * 32 + lane) * 4, v[g][m][a]);
-                            }
-                }
+                    for (int k = 0; k < 2 * W; ++k) {
+                        const int h = k / W, a = k % W;  // stage of the step, atom of the stage
+                        const int atom = h * W * kGroups + (g == 0 ? a : W + a * T::kAtomsN + g - 1);
+                        sts_words4(st + atom * kAtom + lane * 16, v[g * 4][k], v[g * 4 + 1][k],
+                                   v[g * 4 + 2][k], v[g * 4 + 3][k]);
+                    }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -402,7 +451,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * T::kStageBytes);
                     const uint32_t sb = sa + T::kABytes;
-                    const uint32_t ss = smem_u32(sf + (sslot * 2 + h) * T::kScaleBytes);
+                    const uint32_t ss = smem_u32(sf + sslot * T::kStepBytes + h * T::kScaleBytes);
                     const uint32_t slot =
                         tmem_base + static_cast<uint32_t>(T::kAcc * BN + stage * T::kSlotCols);
                     if (elect_one()) {
@@ -579,14 +628,36 @@ static bool encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scales of `rows` rows as a byte matrix; boxes of a step's bytes (`width`) x `box` rows.
+static bool encode_scales(CUtensorMap *map, const uint8_t *scales, int64_t rows, int blocks, int pitch,
+                          int width, int box)
+{
+    auto encode = tensor_map_encoder();
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(blocks), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    cuuint32_t boxes[2] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(box)};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(scales), dims, strides,
+                  boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  width == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, int FMT>
 static cudaError_t gemm_tile(const Fp4Matrix &a, const Fp4Matrix &w, int64_t d_in, Fp4GemmParams p,
                              int64_t tiles, int num_sms, cudaStream_t s)
 {
     using T = f4::Tile<BN, FMT>;
-    CUtensorMap wmap, amap;
+    CUtensorMap wmap, amap, wsmap = {}, asmap = {};
     if (!encode_codes(&wmap, w.codes, p.w_total, d_in, f4::BM) ||
         !encode_codes(&amap, a.codes, a.rows, d_in, BN / 2))
+        return cudaErrorInvalidValue;
+    p.sf_tma = p.scale_pitch % 16 == 0 && ((reinterpret_cast<uintptr_t>(w.scales) |
+                                            reinterpret_cast<uintptr_t>(a.scales)) & 15) == 0;
+    if (p.sf_tma &&
+        (!encode_scales(&wsmap, w.scales, p.w_total, p.blocks, p.scale_pitch, T::kRowBytes, f4::BM) ||
+         !encode_scales(&asmap, a.scales, a.rows, p.blocks, p.scale_pitch, T::kRowBytes, BN)))
         return cudaErrorInvalidValue;
     auto kernel = fp4_gemm_kernel<BN, FMT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -619,7 +690,7 @@ static cudaError_t gemm_tile(const Fp4Matrix &a, const Fp4Matrix &w, int64_t d_i
     }
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * 2 * p.split));
     KernelTimer timer("lnq_fp4_gemm", s);
-    e = cudaLaunchKernelEx(&cfg, kernel, wmap, amap, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, wmap, amap, wsmap, asmap, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

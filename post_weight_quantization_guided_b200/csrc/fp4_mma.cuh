@@ -1,32 +1,11 @@
 // fp4_mma.cuh -- device helpers of the block-scaled 4-bit product: the pair MMA with its
-// descriptors, the scales' copies, and TMEM loads that are waited for together. Inline PTX
+// descriptors, the scales' way to TMEM, and TMEM loads that are waited for together. Inline PTX
 // from the public PTX ISA for sm_100a.
 #pragma once
 
 #include "common.cuh"
 
 namespace lnq {
-
-// Asynchronous global -> shared copy of N (4, 8 or 16) bytes, of which the first `bytes` come from
-// src and the others are zeros.
-template <int N>
-__device__ __forceinline__ void cp_async_zfill(uint32_t dst_smem, const void *src, int bytes)
-{
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem),
-                     "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst_smem),
-                     "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "n"(N)
-                     : "memory");
-}
-// An arrival on `bar` (counted among its expected ones) once this thread's copies so far are done.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
 
 // True in one lane of a converged warp, always the same one.
 __device__ __forceinline__ bool elect_one()
@@ -36,21 +15,34 @@ __device__ __forceinline__ bool elect_one()
     return p != 0u;
 }
 
-// W (2 or 4) consecutive words of shared memory, one word.
-template <int W>
-__device__ __forceinline__ void lds_words(uint32_t (&v)[W], uint32_t addr)
+// N (1 or 2) consecutive words of global memory.
+template <int N>
+__device__ __forceinline__ void ldg_words(uint32_t *v, const uint8_t *src)
 {
-    if constexpr (W == 4)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                     : "r"(addr)
-                     : "memory");
-    else
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+    if constexpr (N == 2) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
+        v[0] = u.x, v[1] = u.y;
+    } else {
+        v[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+    }
 }
-__device__ __forceinline__ void sts_word(uint32_t addr, uint32_t v)
+// Four consecutive words of shared memory.
+__device__ __forceinline__ void lds_words4(uint32_t *v, uint32_t addr)
 {
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void sts_words4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+// Mask of a word's first n bytes (n <= 0: none, n >= 4: all).
+__device__ __forceinline__ uint32_t first_bytes(int n)
+{
+    return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
 }
 
 // Block-scaled product of a pair, kind::mxf4nvf4 (E2M1 operands, two 4-bit elements a byte, K = 64
