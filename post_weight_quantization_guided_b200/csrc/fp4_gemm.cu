@@ -19,8 +19,8 @@
 // a stage. All K-wise bounds are in these copies: codes and scales behind the row's end arrive as
 // zeros.
 //
-// Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8 codes, 9 scales,
-// 10 rearrangement, 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs
+// Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8 loads, 9-10 scales,
+// 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs
 // share the rows' tile.
 // With few tiles, `split` pairs of one cluster take a share of K each and add their sums through
 // distributed shared memory in a fixed order.
@@ -235,39 +235,75 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     const int64_t num_tiles = static_cast<int64_t>(pre[p.experts]) * p.mt;
 
     if (warp == kTmaWarp) {
-        // ------------------------------------------------------------------ codes by TMA
+        // ------------------------------------------------------------------ loads by TMA
+        // One thread serves two rings, whichever has room: codes in stages, and scales in steps of
+        // two stages (8 W bytes of a row: 32 (NV, their 16-byte halves exchanged in every second
+        // four rows: TMA's 32-byte swizzle) or 16 (MX)).
         if (lane == 0) {
-            uint32_t fpar = 0u, fused = 0u;  // per stage: parity of the fills, ever filled
-            int stage = 0;
-            bool ok = true;
-            for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
-                const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
-                const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
-                const int arow = at.b0 + static_cast<int>(cr) * (BN / 2);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&empty[stage], ((fpar >> stage) & 1u) ^ 1u, p.limit)) {
-                        raise_error(err, kErrTimeout, 1);
-                        ok = false;
-                        break;
+            int64_t tile = first, sf_tile = p.sf_tma ? first : num_tiles;
+            int kb = kb0, sf_kb = kb0, stage = 0, slot = 0;
+            uint32_t par = 1u, sf_par = 1u, used = 0u, sf_used = 0u;
+            Fp4TileAt at = {0, 0, 0, 0}, sf_at = {0, 0, 0, 0};
+            if (first < num_tiles)
+                at = sf_at = tile_at<BN>(first, p, lim, pre);
+            long long since = clock64();
+            while (tile < num_tiles || sf_tile < num_tiles) {
+                bool moved = false;
+                if (sf_tile < num_tiles && mbar_test(&sf_empty[slot], sf_par)) {
+                    uint8_t *st = sf + slot * T::kStepBytes;
+                    mbar_arrive_expect_tx(&sf_raw[slot], (BM + BN) * T::kRowBytes);
+                    tma_load_2d(st, &wsmap, &sf_raw[slot], sf_kb * 4 * W,
+                                sf_at.e * p.d_out + sf_at.j0 + static_cast<int>(cr) * BM);
+                    tma_load_2d(st + BM * T::kRowBytes, &asmap, &sf_raw[slot], sf_kb * 4 * W, sf_at.b0);
+                    sf_used |= 1u << slot;
+                    slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                    sf_par ^= slot == 0 ? 1u : 0u;
+                    sf_kb += 2;
+                    if (sf_kb >= kb1) {
+                        sf_kb = kb0;
+                        sf_tile += step;
+                        if (sf_tile < num_tiles)
+                            sf_at = tile_at<BN>(sf_tile, p, lim, pre);
                     }
+                    moved = true;
+                }
+                if (tile < num_tiles && mbar_test(&empty[stage], par)) {
                     uint8_t *st = smem + stage * T::kStageBytes;
                     if (cr == 0)
                         mbar_arrive_expect_tx(&full[stage], 2 * T::kStageBytes);
                     const uint32_t fb = cluster_addr(&full[stage], leader);
-                    tma_load_2d_pair(st, &wmap, fb, kb * 128, wrow);
-                    tma_load_2d_pair(st + T::kABytes, &amap, fb, kb * 128, arow);
-                    fpar ^= 1u << stage;
-                    fused |= 1u << stage;
+                    tma_load_2d_pair(st, &wmap, fb, kb * 128,
+                                     at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM);
+                    tma_load_2d_pair(st + T::kABytes, &amap, fb, kb * 128,
+                                     at.b0 + static_cast<int>(cr) * (BN / 2));
+                    used |= 1u << stage;
                     stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                    par ^= stage == 0 ? 1u : 0u;
+                    if (++kb == kb1) {
+                        kb = kb0;
+                        tile += step;
+                        if (tile < num_tiles)
+                            at = tile_at<BN>(tile, p, lim, pre);
+                    }
+                    moved = true;
+                }
+                if (moved) {
+                    since = clock64();
+                } else if (clock64() - since >= p.limit) {
+                    raise_error(err, kErrTimeout, 1);
+                    break;
                 }
             }
-            if (!ok) {
-                // let this CTA's copies land: the leader waits for the last fill of each stage;
-                // its peer's copies are counted there, so the peer waits a fixed time
+            if (tile < num_tiles || sf_tile < num_tiles) {
+                // Gave up: let this CTA's copies land. The codes' are counted on the leader's
+                // barriers, so the leader waits for the last fill of each and its peer a fixed time.
+                for (int s = 0; s < kScaleRing; ++s)
+                    if ((sf_used >> s) & 1u)
+                        mbar_wait(&sf_raw[s], s < slot ? sf_par ^ 1u : sf_par, kDrainLimit);
                 if (cr == 0) {
                     for (int s = 0; s < T::kStages; ++s)
-                        if ((fused >> s) & 1u)
-                            mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, 1LL << 22);
+                        if ((used >> s) & 1u)
+                            mbar_wait(&full[s], s < stage ? par ^ 1u : par, 1LL << 22);
                 } else {
                     const long long c0 = clock64();
                     while (clock64() - c0 < (1LL << 22)) {
@@ -275,127 +311,104 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 }
             }
         }
-    } else if (warp == kLoadWarp) {
-        // ------------------------------------------------------------------ scales from memory
-        // A step is two stages: 8 W bytes of a row, 32 (NV, their 16-byte halves exchanged in
-        // every second four rows: TMA's 32-byte swizzle) or 16 (MX) bytes of shared memory a row.
-        if (p.sf_tma) {
-            if (lane == 0) {
-                int slot = 0;
-                uint32_t phase = 1u, fused = 0u;
-                bool ok = true;
-                for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
-                    const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
-                    const int wrow = at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM;
-                    for (int kb = kb0; kb < kb1; kb += 2) {
-                        if (!mbar_wait(&sf_empty[slot], phase, p.limit)) {
-                            raise_error(err, kErrTimeout, 2);
-                            ok = false;
-                            break;
-                        }
-                        uint8_t *st = sf + slot * T::kStepBytes;
-                        mbar_arrive_expect_tx(&sf_raw[slot], (BM + BN) * T::kRowBytes);
-                        tma_load_2d(st, &wsmap, &sf_raw[slot], kb * 4 * W, wrow);
-                        tma_load_2d(st + BM * T::kRowBytes, &asmap, &sf_raw[slot], kb * 4 * W, at.b0);
-                        fused |= 1u << slot;
-                        slot = slot + 1 == kScaleRing ? 0 : slot + 1;
-                        phase ^= slot == 0 ? 1u : 0u;
-                    }
+    } else if (warp == kLoadWarp && !p.sf_tma) {
+        // ------------------------------------------------------------------ scales without TMA
+        // Rows that are no multiples of 16 bytes: loads of half a stage's bytes, one step
+        // ahead of their stores, in registers.
+        uint32_t v[kGroups * 4][2 * W];
+        int64_t next_tile = first;
+        int next_kb = kb0;
+        Fp4TileAt at = {0, 0, 0, 0};
+        if (next_tile < num_tiles)
+            at = tile_at<BN>(next_tile, p, lim, pre);
+        auto fetch = [&]() {
+            if (next_tile >= num_tiles)
+                return;
+#pragma unroll
+            for (int g = 0; g < kGroups * 4; ++g) {
+                // rows outside the arrays (nobody reads their sums) repeat the last one
+                const int64_t row = g < 4 ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
+                                                static_cast<int>(cr) * BM + g * 32 + lane
+                                          : static_cast<int64_t>(at.b0) + (g - 4) * 32 + lane;
+                const int64_t top = (g < 4 ? p.w_total : static_cast<int64_t>(p.n)) - 1;
+                const uint8_t *src = (g < 4 ? p.w_scales : p.a_scales) + min(row, top) * p.scale_pitch;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int o = next_kb * 4 * W + u * 2 * W;
+#pragma unroll
+                    for (int k = 0; k < W / 2; ++k)
+                        v[g][u * (W / 2) + k] = 0u;
+                    if (o < p.scale_pitch && (g - 4) * 32 < BN)
+                        ldg_words<W / 2>(v[g] + u * (W / 2), src + o);
                 }
-                if (!ok)  // let the copies land before this CTA exits
-                    for (int s = 0; s < kScaleRing; ++s)
-                        if ((fused >> s) & 1u)
-                            mbar_wait(&sf_raw[s], s < slot ? phase ^ 1u : phase, kDrainLimit);
             }
-        } else {
-            // Rows that are no multiples of 16 bytes: loads of half a stage's bytes, one step
-            // ahead of their stores, in registers.
-            uint32_t v[kGroups * 4][2 * W];
-            int64_t next_tile = first;
-            int next_kb = kb0;
-            Fp4TileAt at = {0, 0, 0, 0};
-            if (next_tile < num_tiles)
-                at = tile_at<BN>(next_tile, p, lim, pre);
-            auto fetch = [&]() {
-                if (next_tile >= num_tiles)
-                    return;
+            next_kb += 2;
+            if (next_kb >= kb1) {
+                next_kb = kb0;
+                next_tile += step;
+                if (next_tile < num_tiles)
+                    at = tile_at<BN>(next_tile, p, lim, pre);
+            }
+        };
+        fetch();
+        int slot = 0;
+        uint32_t phase = 1u;
+        bool ok = true;
+        for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+            for (int kb = kb0; kb < kb1; kb += 2) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase, p.limit))) {
+                    if (lane == 0)
+                        raise_error(err, kErrTimeout, 2);
+                    ok = false;
+                    break;
+                }
+                const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
 #pragma unroll
                 for (int g = 0; g < kGroups * 4; ++g) {
-                    // rows outside the arrays (nobody reads their sums) repeat the last one
-                    const int64_t row = g < 4 ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
-                                                    static_cast<int>(cr) * BM + g * 32 + lane
-                                              : static_cast<int64_t>(at.b0) + (g - 4) * 32 + lane;
-                    const int64_t top = (g < 4 ? p.w_total : static_cast<int64_t>(p.n)) - 1;
-                    const uint8_t *src = (g < 4 ? p.w_scales : p.a_scales) + min(row, top) * p.scale_pitch;
+                    if ((g - 4) * 32 >= BN)
+                        continue;
+                    uint32_t *w = v[g];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int o = next_kb * 4 * W + u * 2 * W;
+                    for (int k = 0; k < 2 * W; ++k)  // nothing behind the row's last block
+                        w[k] &= first_bytes(p.blocks - kb * 4 * W - 4 * k);
 #pragma unroll
-                        for (int k = 0; k < W / 2; ++k)
-                            v[g][u * (W / 2) + k] = 0u;
-                        if (o < p.scale_pitch && (g - 4) * 32 < BN)
-                            ldg_words<W / 2>(v[g] + u * (W / 2), src + o);
-                    }
+                    for (int c = 0; c < W / 2; ++c)
+                        sts_words4(st + T::chunk_at(g * 32 + lane, c), w[4 * c], w[4 * c + 1],
+                                   w[4 * c + 2], w[4 * c + 3]);
                 }
-                next_kb += 2;
-                if (next_kb >= kb1) {
-                    next_kb = kb0;
-                    next_tile += step;
-                    if (next_tile < num_tiles)
-                        at = tile_at<BN>(next_tile, p, lim, pre);
-                }
-            };
-            fetch();
-            int slot = 0;
-            uint32_t phase = 1u;
-            bool ok = true;
-            for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
-                for (int kb = kb0; kb < kb1; kb += 2) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase, p.limit))) {
-                        if (lane == 0)
-                            raise_error(err, kErrTimeout, 2);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
-#pragma unroll
-                    for (int g = 0; g < kGroups * 4; ++g) {
-                        if ((g - 4) * 32 >= BN)
-                            continue;
-                        uint32_t *w = v[g];
-#pragma unroll
-                        for (int k = 0; k < 2 * W; ++k)  // nothing behind the row's last block
-                            w[k] &= first_bytes(p.blocks - kb * 4 * W - 4 * k);
-#pragma unroll
-                        for (int c = 0; c < W / 2; ++c)
-                            sts_words4(st + T::chunk_at(g * 32 + lane, c), w[4 * c], w[4 * c + 1],
-                                       w[4 * c + 2], w[4 * c + 3]);
-                    }
-                    mbar_arrive(&sf_raw[slot]);
-                    fetch();
-                    slot = slot + 1 == kScaleRing ? 0 : slot + 1;
-                    phase ^= slot == 0 ? 1u : 0u;
-                }
+                mbar_arrive(&sf_raw[slot]);
+                fetch();
+                slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                phase ^= slot == 0 ? 1u : 0u;
             }
         }
-    } else if (warp == kScaleWarp) {
+    } else if (warp == kScaleWarp || warp == kLoadWarp) {
         // ------------------------------------------------------------------ scales into atoms
         // Lane l takes rows l, l + 32, l + 64, l + 96 of each 128 and writes, for each word of
         // the rows, the four rows' words as 16 bytes of the word's atom: in place, so everything is
-        // read before anything is written.
+        // read before anything is written. Two warps take turns where TMA loads the scales.
         const uint32_t ready_leader = cluster_addr(&sf_ready[0], leader);
-        int slot = 0;
+        const int turns = p.sf_tma ? 2 : 1, my_turn = warp == kScaleWarp ? 0 : 1;
+        int slot = 0, turn = 0;
         uint32_t phase = 0u;
         bool ok = true;
         for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
             for (int kb = kb0; kb < kb1; kb += 2) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&sf_raw[slot], phase, p.limit))) {
+                const int at_slot = slot;
+                const uint32_t at_phase = phase;
+                const bool mine = turn == my_turn;
+                slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                phase ^= slot == 0 ? 1u : 0u;
+                turn = turn + 1 == turns ? 0 : turn + 1;
+                if (!mine)
+                    continue;
+                if (!__all_sync(0xffffffffu, mbar_wait(&sf_raw[at_slot], at_phase, p.limit))) {
                     if (lane == 0)
                         raise_error(err, kErrTimeout, 3);
                     ok = false;
                     break;
                 }
-                const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
+                const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(at_slot * T::kStepBytes);
                 uint32_t v[kGroups * 4][2 * W];
 #pragma unroll
                 for (int g = 0; g < kGroups * 4; ++g)
@@ -412,12 +425,14 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                         sts_words4(st + atom * kAtom + lane * 16, v[g * 4][k], v[g * 4 + 1][k],
                                    v[g * 4 + 2][k], v[g * 4 + 3][k]);
                     }
+                // After the fence every lane's stores are in this CTA's shared memory, where the
+                // tensor core reads them. The arrival is sent behind it, without a release at
+                // cluster scope: that would also wait for all other writes of this SM (the
+                // epilogue's stores to global memory), at 0.3 us a step.
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(ready_leader + static_cast<uint32_t>(slot * 8));
-                slot = slot + 1 == kScaleRing ? 0 : slot + 1;
-                phase ^= slot == 0 ? 1u : 0u;
+                    mbar_arrive_remote(ready_leader + static_cast<uint32_t>(at_slot * 8));
             }
         }
     } else if (warp == kMmaWarp) {

@@ -15,6 +15,27 @@ __device__ __forceinline__ bool elect_one()
     return p != 0u;
 }
 
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
+
+// Arrive on an mbarrier of a CTA of the cluster, after what this thread did before in its own CTA
+// (release at CTA scope).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr)
+                 : "memory");
+}
+
 // N (1 or 2) consecutive words of global memory.
 template <int N>
 __device__ __forceinline__ void ldg_words(uint32_t *v, const uint8_t *src)
