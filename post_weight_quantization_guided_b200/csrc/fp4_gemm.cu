@@ -437,16 +437,13 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------ MMA issue (leader)
-        // The whole warp waits, one elected lane issues (always the same one: the warp stays
-        // converged), so that operands stay in uniform registers.
-        if (cr == 0) {
+        if (cr == 0 && elect_one()) {
             constexpr bool kNv = FMT == LNQ_FP4_NV;
-            int stage = 0, it = 0, sslot = 0;
-            uint32_t fph = 0u, sphase = 0u;  // phase parities
+            int stage = 0, slot = 0, acc = 0;
+            uint32_t fph = 0u, sph = 0u, aph = 1u;  // parities: codes, scales, accumulators
             bool ok = true;
-            for (int64_t tile = first; tile < num_tiles && ok; tile += step, ++it) {
-                const int acc = it % T::kAcc, use = it / T::kAcc;
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], (use & 1) ^ 1, p.limit))) {
+            for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
+                if (!mbar_wait_cluster(&tempty[acc], aph, p.limit)) {
                     raise_error(err, kErrTimeout, 4);
                     ok = false;
                     break;
@@ -455,55 +452,48 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     const int h = (kb - kb0) & 1;  // stage of the step
-                    if (!__all_sync(0xffffffffu,
-                                    (h == 1 || mbar_wait_cluster(&sf_ready[sslot], sphase, p.limit)) &&
-                                        mbar_wait(&full[stage], (fph >> stage) & 1u, p.limit))) {
+                    if ((h == 0 && !mbar_wait_cluster(&sf_ready[slot], sph, p.limit)) ||
+                        !mbar_wait(&full[stage], fph, p.limit)) {
                         raise_error(err, kErrTimeout, 5);
                         ok = false;
                         break;
                     }
-                    fph ^= 1u << stage;
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * T::kStageBytes);
-                    const uint32_t sb = sa + T::kABytes;
-                    const uint32_t ss = smem_u32(sf + sslot * T::kStepBytes + h * T::kScaleBytes);
-                    const uint32_t slot =
+                    const uint64_t ad = umma_desc_sw128(sa, 16, 1024);
+                    const uint64_t bd = umma_desc_sw128(sa + T::kABytes, 16, 1024);
+                    const uint64_t sd = smem_desc_plain(
+                        smem_u32(sf + slot * T::kStepBytes + h * T::kScaleBytes));
+                    const uint32_t st =
                         tmem_base + static_cast<uint32_t>(T::kAcc * BN + stage * T::kSlotCols);
-                    if (elect_one()) {
 #pragma unroll
-                        for (int c = 0; c < T::kAtomsK * (1 + T::kAtomsN); ++c)
-                            tmem_cp_32x128b_pair(slot + c * 4, smem_desc_plain(ss + c * kAtom));
+                    for (int c = 0; c < T::kAtomsK * (1 + T::kAtomsN); ++c)
+                        tmem_cp_32x128b_pair(st + c * 4, sd + c * (kAtom >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < BK / 64; ++kk) {
-                            const int atom = kNv ? kk : kk / 2;
-                            const uint32_t idesc = umma_idesc_f4(PM, BN, !kNv, kNv ? 0u : (kk & 1) * 2u);
-                            const uint64_t ad = umma_desc_sw128(sa + kk * 32, 16, 1024);
-                            const uint64_t bd = umma_desc_sw128(sb + kk * 32, 16, 1024);
-                            umma_f4_pair<kNv>(d_tmem, ad, bd, idesc, slot + atom * 4,
-                                              slot + (T::kAtomsK + atom * T::kAtomsN) * 4,
-                                              (kb != kb0 || kk != 0) ? 1u : 0u);
-                        }
-                        umma_commit_pair(&empty[stage], pair_mask);
-                        if (h == 1 || kb + 1 == kb1)
-                            umma_commit_pair(&sf_empty[sslot], pair_mask);
+                    for (int kk = 0; kk < BK / 64; ++kk) {  // 32 bytes of K each
+                        const int atom = kNv ? kk : kk / 2;
+                        const uint32_t idesc = umma_idesc_f4(PM, BN, !kNv, kNv ? 0u : (kk & 1) * 2u);
+                        umma_f4_pair<kNv>(d_tmem, ad + kk * 2, bd + kk * 2, idesc, st + atom * 4,
+                                          st + (T::kAtomsK + atom * T::kAtomsN) * 4,
+                                          (kb != kb0 || kk != 0) ? 1u : 0u);
                     }
-                    __syncwarp();
+                    umma_commit_pair(&empty[stage], pair_mask);
                     if (h == 1 || kb + 1 == kb1) {
-                        sslot = sslot + 1 == kScaleRing ? 0 : sslot + 1;
-                        sphase ^= sslot == 0 ? 1u : 0u;
+                        umma_commit_pair(&sf_empty[slot], pair_mask);
+                        slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+                        sph ^= slot == 0 ? 1u : 0u;
                     }
                     stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                    fph ^= stage == 0 ? 1u : 0u;
                 }
                 if (!ok)
                     break;
-                if (elect_one())
-                    umma_commit_pair(&tfull[acc], pair_mask);
-                __syncwarp();
+                umma_commit_pair(&tfull[acc], pair_mask);
+                acc = acc + 1 == T::kAcc ? 0 : acc + 1;
+                aph ^= acc == 0 ? 1u : 0u;
             }
-            // every MMA of this warp has completed once `drain` flips
-            if (elect_one())
-                umma_commit_pair(drain, static_cast<uint16_t>(1u << leader));
-            __syncwarp();
+            // every MMA of this thread has completed once `drain` flips
+            umma_commit_pair(drain, static_cast<uint16_t>(1u << leader));
             mbar_wait(drain, 0, kDrainLimit);
         }
     } else {
@@ -544,8 +534,8 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 tmem_ld_fence(v[c]);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(tempty_leader + static_cast<uint32_t>(acc * 8));
+            if (lane == 0)  // what it orders are TMEM reads: no release at cluster scope
+                mbar_arrive_remote(tempty_leader + static_cast<uint32_t>(acc * 8));
             if (p.split > 1) {
                 // this pair's share of the sums, [row][128 outputs], over the finished stages
                 float *sums = reinterpret_cast<float *>(smem);
