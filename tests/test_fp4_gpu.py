@@ -282,6 +282,33 @@ def test_gemv_32_bit_activations_are_not_rounded(lnq):
     assert torch.equal(y, x.sum(1, keepdim=True).expand(3, 4))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 11])
+def test_gemv_extreme_mx_scales(lnq, dtype, n):
+    """Scales from the whole range of powers of two, mixed within rows; the products stay in range
+    through x. Bits of x below 2^-133 and results below the 32-bit normal range may be cut off."""
+    rng = _rng(13, n)
+    d_in, d_out = 416, 24
+    codes, scales = ref.random_stored(rng, (d_out,), d_in, MX)
+    scales[:, :13] = np.where(rng.random((d_out, 13)) < 0.6, rng.integers(100, 130, (d_out, 13)),
+                              rng.integers(0, 255, (d_out, 13)))
+    scales[3, :13], scales[4, :13], scales[5, 1:13] = 0, 254, 1
+    block = np.arange(d_in) // 32
+    x = rng.standard_normal((n, d_in)) * 2.0 ** rng.integers(-20, 3, 13)[block]
+    xt = dev(x, dtype)
+    w = ref.values(codes, scales, d_in, MX)
+    y = f64(lnq.lnq_fp4_gemv(xt, dev(codes), dev(scales), MX, dtype=torch.float32))
+    want = f64(xt) @ w.T
+    S = np.abs(f64(xt)) @ np.abs(w).T
+    top = float(torch.finfo(torch.float32).max)
+    sure = S < top / 2  # no partial sum overflows
+    tol = (d_in + 4) * 2.0 ** -23 * S + 2.0 ** -126
+    assert sure.mean() > 0.3
+    assert (np.abs(y - want) <= tol)[sure].all()
+    with np.errstate(invalid="ignore"):
+        assert (np.isinf(y) | np.isnan(y) | (np.abs(y - want) <= tol))[~sure].all()
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 def test_products_with_nan_scales(lnq, fmt):
     """A NaN block of one row of either operand makes that row's (column's) outputs NaN, no other."""
@@ -343,6 +370,57 @@ def test_gemm(lnq, fmt, out, n, d_in, d_out, exact):
                          dtype=out)
     scale = 1.0 if ta is None else float(np.float32(ta)) * float(np.float32(tb))
     check_product(y, ref.values(ac, as_, d_in, fmt), ref.values(wc, ws, d_in, fmt), scale, exact)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("n,d_in,d_out", [(2100, 700, 5000), (5000, 256, 1100), (31, 900, 20000),
+                                          (100, 2944, 9000), (60, 1408, 12000), (1300, 11008, 777)])
+def test_gemm_many_tiles(lnq, fmt, n, d_in, d_out):
+    """More tiles than run at once, for every tile width and both ways of loading scales; equality
+    on exact sums, in 64 bits on the device."""
+    rng = _rng(n, d_in, d_out, 2)
+    ac, as_ = ref.random_stored(rng, (n,), d_in, fmt, True)
+    ac &= 0x33
+    as_[:] = 127 if fmt == MX else 56
+    if d_in > 4000:
+        ac &= 0x11
+    wc, ws = ref.random_stored(rng, (d_out,), d_in, fmt, True)
+    x = dev(ref.values(ac, as_, d_in, fmt))
+    want = x @ dev(ref.values(wc, ws, d_in, fmt)).T
+    assert want.abs().max() < 2 ** 20
+    y = lnq.lnq_fp4_gemm(dev(ac), dev(as_), dev(wc), dev(ws), d_in, fmt, dtype=torch.float32)
+    assert torch.equal(y.double(), want)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_grouped_gemm_many_tiles(lnq, fmt):
+    rng = _rng(34)
+    E, d_in, d_out = 9, 520, 1500
+    sizes = [300, 0, 1, 1700, 128, 129, 33, 700, 64]
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    n = int(off[-1])
+    ac, as_ = ref.random_stored(rng, (n,), d_in, fmt, True)
+    ac &= 0x33
+    as_[:] = 127 if fmt == MX else 56
+    wc, ws = ref.random_stored(rng, (E, d_out), d_in, fmt, True)
+    x = dev(ref.values(ac, as_, d_in, fmt))
+    y = lnq.lnq_fp4_grouped_gemm(dev(ac), dev(as_), dev(off), dev(wc), dev(ws), d_in, fmt,
+                                 dtype=torch.float32)
+    for e in range(E):
+        want = x[off[e]:off[e + 1]] @ dev(ref.values(wc[e], ws[e], d_in, fmt)).T
+        assert torch.equal(y[off[e]:off[e + 1]].double(), want)
+
+
+def test_gemm_extreme_mx_scales(lnq):
+    """Small scales on one side against large ones on the other."""
+    rng = _rng(14)
+    n, d_in, d_out = 20, 512, 140
+    ac, as_ = ref.random_stored(rng, (n,), d_in, MX)
+    wc, ws = ref.random_stored(rng, (d_out,), d_in, MX)
+    as_[:, :16] = rng.integers(0, 12, (n, 16))
+    ws[:, :16] = rng.integers(242, 255, (d_out, 16))
+    y = lnq.lnq_fp4_gemm(dev(ac), dev(as_), dev(wc), dev(ws), d_in, MX, dtype=torch.float32)
+    check_product(y, ref.values(ac, as_, d_in, MX), ref.values(wc, ws, d_in, MX))
 
 
 def test_gemm_writes_only_its_columns(lnq):
