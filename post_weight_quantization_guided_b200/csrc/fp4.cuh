@@ -89,7 +89,7 @@ cudaError_t fp4_dequantize_launch(const uint8_t *codes, const uint8_t *scales, i
 // offsets == nullptr: one group of all n rows and one matrix.
 cudaError_t fp4_gemv_launch(const void *x, int xt, int64_t n, int64_t ldx, const int32_t *offsets,
                             int64_t experts, const Fp4Matrix &w, int64_t d_in, int fmt, void *y,
-                            int yt, int64_t ldy, cudaStream_t s);
+                            int yt, int64_t ldy, int num_sms, cudaStream_t s);
 cudaError_t fp4_gemm_launch(const Fp4Matrix &a, const int32_t *offsets, int64_t experts,
                             const Fp4Matrix &w, int64_t d_in, int fmt, void *y, int yt,
                             int64_t ldy, long long wait_limit, int num_sms, cudaStream_t s);

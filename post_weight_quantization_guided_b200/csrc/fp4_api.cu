@@ -55,7 +55,7 @@ lnq_status gemv(const void *x, int xt, int64_t n, int64_t ldx, const int32_t *of
         return LNQ_OK;
     return status_of(fp4_gemv_launch(x, xt, n, ldx, offsets, experts,
                                      Fp4Matrix{codes, scales, t, d_out}, d_in, fmt, y, yt, ldy,
-                                     reinterpret_cast<cudaStream_t>(stream)));
+                                     device_sm_count(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 lnq_status gemm(const uint8_t *a_codes, const uint8_t *a_scales, const float *ta, int64_t n,

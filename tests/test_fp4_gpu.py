@@ -309,6 +309,17 @@ def test_gemv_extreme_mx_scales(lnq, dtype, n):
         assert (np.isinf(y) | np.isnan(y) | (np.abs(y - want) <= tol))[~sure].all()
 
 
+@pytest.mark.parametrize("byte", [0, 1, 2, 8, 9, 130, 131, 253, 254])
+def test_gemv_smallest_and_largest_mx_scales(lnq, byte):
+    """Whole rows at one end of the scales, against x at the other end: equal on exact sums."""
+    rng = _rng(15, byte)
+    codes, scales = ref.random_stored(rng, (20,), 300, MX)
+    scales[:, :10] = byte
+    x = rng.integers(-2, 3, (3, 300)) * 2.0 ** (100 if byte < 127 else -100)
+    y = lnq.lnq_fp4_gemv(dev(x, torch.bfloat16), dev(codes), dev(scales), MX, dtype=torch.float32)
+    check_product(y, x, ref.values(codes, scales, 300, MX), exact=True)
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 def test_products_with_nan_scales(lnq, fmt):
     """A NaN block of one row of either operand makes that row's (column's) outputs NaN, no other."""
