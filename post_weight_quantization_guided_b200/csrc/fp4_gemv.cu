@@ -21,8 +21,10 @@
 // leaves code * s times a power of two (taken out of the finished sum). The order of elements within the
 // instruction's K is free, and x is paired alike.
 //
-// With few outputs the CTAs of a cluster take shares of K and add their sums in order through
-// distributed shared memory.
+// With few tiles several warps of a CTA share a tile's K, and where x does not fit its shared
+// memory several CTAs of a cluster do; the sums are added in order.
+#include <atomic>
+
 #include "fp4.cuh"
 #include "profile.cuh"
 
@@ -72,24 +74,33 @@ __device__ __forceinline__ uint32_t twice_bf16(float v)
     return h | (h << 16);
 }
 
-// Piece p of v (p < pieces): the leading 8 bits, the next 8, the last 8. An infinity is all in
-// piece 0; a NaN is in the last.
-__device__ __forceinline__ uint32_t piece_bits(float v, int p)
+// The pieces of v, as bf16 bits: the leading 8 bits, the next 8, the last 8. An infinity is all in
+// the first; a NaN is in the last too.
+template <int P>
+__device__ __forceinline__ void split_bf16(float v, uint32_t (&bits)[P])
 {
-    const float a = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-    if (p == 0)
-        return __float_as_uint(a) >> 16;
-    const float r = fabsf(v) == __uint_as_float(0x7F800000u) ? 0.f : v - a;
-    const float b = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
-    return __float_as_uint(p == 1 ? (isnan(r) ? r : b) : r - b) >> 16;
+    bits[0] = __float_as_uint(v) >> 16;
+    if constexpr (P > 1) {
+        const float r = fabsf(v) == __uint_as_float(0x7F800000u)
+                            ? 0.f
+                            : v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+        if constexpr (P == 2) {
+            bits[1] = __float_as_uint(r) >> 16;  // of a 16-bit v the rest has 3 bits
+        } else {
+            const float b = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
+            bits[1] = __float_as_uint(b) >> 16;
+            bits[2] = __float_as_uint(r - b) >> 16;
+        }
+    }
 }
 
-// x[0..7] (zeros from element `left` on) as one word's part of the instruction's column: register i
-// holds elements i and i + 4, of piece p.
+// x[0..7] (zeros from element `left` on) as one word's part of the instruction's columns, one for
+// each piece: register i holds elements i and i + 4.
 template <typename TX>
-__device__ __forceinline__ void load_column(const TX *__restrict__ x, int left, bool wide, int p,
-                                            uint32_t (&b)[4])
+__device__ __forceinline__ void load_columns(const TX *__restrict__ x, int left, bool wide,
+                                             uint4 (&col)[gv::Pieces<TX>::n])
 {
+    constexpr int P = gv::Pieces<TX>::n;
     alignas(16) TX e[8];
     if (wide && left >= 8) {
 #pragma unroll
@@ -100,16 +111,19 @@ __device__ __forceinline__ void load_column(const TX *__restrict__ x, int left, 
         for (int k = 0; k < 8; ++k)
             e[k] = k < left ? x[k] : from_f32<TX>(0.f);
     }
-    if constexpr (gv::Pieces<TX>::n == 1) {
+    if constexpr (P == 1) {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(e);
-        b[0] = __byte_perm(w[0], w[2], 0x5410);
-        b[1] = __byte_perm(w[0], w[2], 0x7632);
-        b[2] = __byte_perm(w[1], w[3], 0x5410);
-        b[3] = __byte_perm(w[1], w[3], 0x7632);
+        col[0] = make_uint4(__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632),
+                            __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632));
     } else {
+        uint32_t b[8][P];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            b[i] = piece_bits(to_f32<TX>(e[i]), p) | (piece_bits(to_f32<TX>(e[i + 4]), p) << 16);
+        for (int k = 0; k < 8; ++k)
+            split_bf16<P>(to_f32<TX>(e[k]), b[k]);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            col[p] = make_uint4(b[0][p] | (b[4][p] << 16), b[1][p] | (b[5][p] << 16),
+                                b[2][p] | (b[6][p] << 16), b[3][p] | (b[7][p] << 16));
     }
 }
 
@@ -156,79 +170,106 @@ __device__ __forceinline__ uint32_t scale_rest(uint32_t v)
 }
 
 // NT column tiles (of 8 / pieces rows of x) per pass over the weights. Grid: x = clusters per
-// expert times the cluster's CTAs, y = experts.
+// expert times the cluster's CTAs, y = experts. `parts` warps share a tile's K within a CTA,
+// `shares` CTAs within a cluster; `panel` chunks of x fit at a time.
 template <typename TX, int FMT, int NT>
 __global__ void __launch_bounds__(gv::kThreads, 2)
     fp4_gemv_kernel(const TX *__restrict__ x, int n, int64_t ldx, bool wide,
                     const int32_t *__restrict__ offsets, Fp4Matrix w, int d_in, void *__restrict__ y,
-                    int yt, int64_t ldy, int shares, int panel)
+                    int yt, int64_t ldy, int parts, int shares, int panel)
 {
     using namespace gv;
     constexpr int P = Pieces<TX>::n, kTok = 8 / P;   // rows of x per column tile
     constexpr int kPass = NT * kTok;                 // and per pass
     constexpr int kBlocks = 32 / fp4_block(FMT);     // blocks of a lane's 32 elements
-    extern __shared__ uint4 xs[];                    // [panel][NT][4 words][32 lanes]
+    // With one column tile the multipliers come from a table (83 us where computing them takes
+    // 87, 16 rows over 8 experts 4096 -> 14336); with more, shared memory is busy with x (69 and 54).
+    constexpr bool kTable = NT == 1;
+    extern __shared__ uint4 xs[];                    // [panel][NT][4 words][4 lanes t][columns]
     __shared__ float sums[kWarps][kRows][NT * 8 + 1];
+    __shared__ uint32_t multiplier[kTable ? 256 : 1];  // of each scale byte
     const int e = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int2 rows = offsets == nullptr ? make_int2(0, n) : fp4_group_rows(offsets, e, n);
     if (rows.x >= rows.y)
         return;
+    if (kTable)
+        multiplier[threadIdx.x] = scale_pair<FMT>(threadIdx.x);
     const int share = shares > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int cluster = static_cast<int>(blockIdx.x) / shares, clusters = static_cast<int>(gridDim.x) / shares;
     const int d_out = static_cast<int>(w.rows), tiles = (d_out + kRows - 1) / kRows;
     const int64_t code_pitch = fp4_code_pitch(d_in), scale_pitch = fp4_scale_pitch(d_in, FMT);
     const int chunks = (d_in + kChunk - 1) / kChunk;
-    const int blocks = (d_in + fp4_block(FMT) - 1) / fp4_block(FMT);
     const int c_begin = static_cast<int>(static_cast<int64_t>(share) * chunks / shares);
     const int c_end = static_cast<int>(static_cast<int64_t>(share + 1) * chunks / shares);
+    // this lane's scale bytes of the last chunk: zeros behind the row's last block
+    const int left_blocks = (d_in - (chunks - 1) * kChunk - t * 32 + fp4_block(FMT) - 1) / fp4_block(FMT);
+    const uint32_t tail = left_blocks >= kBlocks ? 0xFFFFu : (left_blocks == 1 ? 0xFFu : 0u);
     const int64_t first = static_cast<int64_t>(e) * d_out;
     const float scale = (w.t == nullptr ? 1.f : __ldg(w.t + e)) * kUnshift<FMT>;
-    // this warp's tiles: tile0, tile0 + hop, ...; the CTA's rounds
-    const int tile0 = cluster + warp * clusters, hop = kWarps * clusters;
-    const int rounds = (tiles - cluster + hop - 1) / hop;
+    // a round: kWarps / parts tiles of this CTA, every clusters-th of the matrix
+    const int slots = kWarps / parts, slot = warp / parts, part = warp % parts;
+    const int rounds = ((tiles - cluster + clusters - 1) / clusters + slots - 1) / slots;
     const bool once = c_end - c_begin <= panel;  // x fits at once
+    // columns in use: one tile of few rows keeps only those
+    const int tokens = NT > 1 ? kTok : min(kTok, rows.y - rows.x), columns = NT > 1 ? 8 : tokens * P;
 
     for (int b0 = rows.x; b0 < rows.y; b0 += kPass) {
         auto stage = [&](int c0, int c1) {  // x of chunks c0 .. c1 - 1
-            for (int i = threadIdx.x; i < (c1 - c0) * NT * 128; i += kThreads) {
-                const int c = i / (NT * 128), nt = i / 128 % NT, j = (i >> 5) & 3, l = i & 31;
-                const int col = l >> 2, b = b0 + nt * kTok + col / P;
-                const int k = (c0 + c) * kChunk + (l & 3) * 32 + j * 8;
-                const int left = col < kTok * P && b < rows.y ? d_in - k : 0;
-                uint32_t v[4];
-                load_column<TX>(x + (left > 0 ? b * ldx + k : 0), left, wide, col % P, v);
-                xs[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int i = threadIdx.x; i < (c1 - c0) * NT * 16 * tokens; i += kThreads) {
+                const int q = i / tokens, token = i - q * tokens;  // q: [chunk][nt][word][t]
+                const int c = q / (NT * 16), nt = q / 16 % NT, b = b0 + nt * kTok + token;
+                const int k = (c0 + c) * kChunk + (q & 3) * 32 + (q >> 2 & 3) * 8;
+                if (b >= rows.y)  // nobody reads its sums
+                    continue;
+                uint4 col[P];
+                load_columns<TX>(x + (k < d_in ? b * ldx + k : 0), d_in - k, wide, col);
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    xs[q * columns + token * P + p] = col[p];
             }
         };
-        __syncthreads();  // the last pass has read x
+        __syncthreads();  // the last pass has read x; the multipliers are written
         if (once) {
             stage(c_begin, c_end);
             __syncthreads();
         }
-        for (int round = 0; round < rounds; ++round) {
-            const int tile = tile0 + round * hop;
-            const bool mine = tile < tiles;
+        const uint8_t *codes0, *codes1, *scales0, *scales1;
+        Chunk ring[kAhead];
+        auto fetch = [&](Chunk &q, int ahead, int left) {
+            if (left <= 0)
+                return;
+            q.q0 = __ldg(reinterpret_cast<const uint4 *>(codes0 + ahead * 64));
+            q.q1 = __ldg(reinterpret_cast<const uint4 *>(codes1 + ahead * 64));
+            if (kBlocks == 2) {
+                q.s0 = __ldg(reinterpret_cast<const uint16_t *>(scales0 + ahead * 8));
+                q.s1 = __ldg(reinterpret_cast<const uint16_t *>(scales1 + ahead * 8));
+            } else {
+                q.s0 = __ldg(scales0 + ahead * 4);
+                q.s1 = __ldg(scales1 + ahead * 4);
+            }
+        };
+        auto tile_of = [&](int round) { return cluster + (round * slots + slot) * clusters; };
+        // the first chunks of this warp's part of chunks p0 .. p1 - 1 of a tile
+        auto begin = [&](int tile, int p0, int p1) {
+            if (tile >= tiles)
+                return;
+            const int w_begin = p0 + part * (p1 - p0) / parts, w_end = p0 + (part + 1) * (p1 - p0) / parts;
             // outputs behind the last (nobody writes their sums) repeat it
-            const int j0 = tile * kRows;
-            const int64_t r0 = first + min(j0 + g, d_out - 1), r1 = first + min(j0 + g + 8, d_out - 1);
-            const uint8_t *codes0 = w.codes + r0 * code_pitch + t * 16;
-            const uint8_t *codes1 = w.codes + r1 * code_pitch + t * 16;
-            const uint8_t *scales0 = w.scales + r0 * scale_pitch + t * kBlocks;
-            const uint8_t *scales1 = w.scales + r1 * scale_pitch + t * kBlocks;
-            auto fetch = [&](Chunk &q, int c, int c1) {
-                if (c >= c1)
-                    return;
-                q.q0 = __ldg(reinterpret_cast<const uint4 *>(codes0 + static_cast<int64_t>(c) * 64));
-                q.q1 = __ldg(reinterpret_cast<const uint4 *>(codes1 + static_cast<int64_t>(c) * 64));
-                if (kBlocks == 2) {
-                    q.s0 = __ldg(reinterpret_cast<const uint16_t *>(scales0 + c * 8));
-                    q.s1 = __ldg(reinterpret_cast<const uint16_t *>(scales1 + c * 8));
-                } else {
-                    q.s0 = __ldg(scales0 + c * 4);
-                    q.s1 = __ldg(scales1 + c * 4);
-                }
-            };
+            const int64_t r0 = first + min(tile * kRows + g, d_out - 1);
+            const int64_t r1 = first + min(tile * kRows + g + 8, d_out - 1);
+            codes0 = w.codes + r0 * code_pitch + static_cast<int64_t>(w_begin) * 64 + t * 16;
+            codes1 = w.codes + r1 * code_pitch + static_cast<int64_t>(w_begin) * 64 + t * 16;
+            scales0 = w.scales + r0 * scale_pitch + (w_begin * 4 + t) * kBlocks;
+            scales1 = w.scales + r1 * scale_pitch + (w_begin * 4 + t) * kBlocks;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                fetch(ring[u], u, w_end - w_begin - u);
+        };
+        if (once)
+            begin(tile_of(0), c_begin, c_end);
+        for (int round = 0; round < rounds; ++round) {
+            const bool mine = tile_of(round) < tiles;
             float acc[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -241,40 +282,41 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                     __syncthreads();
                     stage(p0, p1);
                     __syncthreads();
+                    begin(tile_of(round), p0, p1);
                 }
                 if (!mine)
                     continue;
-                Chunk ring[kAhead];
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    fetch(ring[u], p0 + u, p1);
-                for (int cc = p0; cc < p1; cc += kAhead) {
+                const int w_begin = p0 + part * (p1 - p0) / parts, w_end = p0 + (part + 1) * (p1 - p0) / parts;
+                const uint4 *xc = xs + (w_begin - p0) * (NT * 16) * columns + t * columns + min(g, columns - 1);
+                const bool has = g < columns;
+                for (int c0 = w_begin; c0 < w_end; c0 += kAhead) {
 #pragma unroll
                     for (int u = 0; u < kAhead; ++u) {
-                        const int c = cc + u;
-                        if (c >= p1)
+                        const int c = c0 + u;
+                        if (c >= w_end)
                             break;
-                        const Chunk q = ring[u];
-                        fetch(ring[u], c + kAhead, p1);
-                        const uint32_t w0[4] = {q.q0.x, q.q0.y, q.q0.z, q.q0.w};
-                        const uint32_t w1[4] = {q.q1.x, q.q1.y, q.q1.z, q.q1.w};
-                        const int block0 = c * (kChunk / fp4_block(FMT)) + t * kBlocks;
-                        const uint4 *xc = xs + (c - p0) * (NT * 128) + lane;
+                        Chunk &q = ring[u];
+                        if (c == chunks - 1) {
+                            q.s0 &= tail;
+                            q.s1 &= tail;
+                        }
                         uint32_t m0[kBlocks], m1[kBlocks];
 #pragma unroll
                         for (int k = 0; k < kBlocks; ++k) {
-                            const bool in = block0 + k < blocks;  // else behind the row
-                            m0[k] = in ? scale_pair<FMT>((q.s0 >> (8 * k)) & 255u) : 0u;
-                            m1[k] = in ? scale_pair<FMT>((q.s1 >> (8 * k)) & 255u) : 0u;
+                            const uint32_t v0 = (q.s0 >> (8 * k)) & 255u, v1 = (q.s1 >> (8 * k)) & 255u;
+                            m0[k] = kTable ? multiplier[v0] : scale_pair<FMT>(v0);
+                            m1[k] = kTable ? multiplier[v1] : scale_pair<FMT>(v1);
                         }
                         const bool large = FMT == LNQ_FP4_MX &&
                                            __any_sync(0xffffffffu, max(q.s0, q.s1) > kTopScale);
+                        const uint32_t h0 = large ? scale_rest(q.s0) : 0u, h1 = large ? scale_rest(q.s1) : 0u;
+                        const uint32_t w0[4] = {q.q0.x, q.q0.y, q.q0.z, q.q0.w};
+                        const uint32_t w1[4] = {q.q1.x, q.q1.y, q.q1.z, q.q1.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t lo[4], hi[4];
                             decode_word(w0[j], w1[j], m0[j * kBlocks / 4], m1[j * kBlocks / 4], lo, hi);
                             if (large) {
-                                const uint32_t h0 = scale_rest(q.s0), h1 = scale_rest(q.s1);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     lo[k] = mul_bf16x2(lo[k], k & 1 ? h1 : h0);
@@ -283,14 +325,24 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                const uint4 v = xc[nt * 128 + j * 32];
+                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                if (NT > 1 || has)
+                                    v = xc[(nt * 16 + j * 4) * columns];
                                 mma_bf16(acc[nt], lo, v.x, v.y);
                                 mma_bf16(acc[nt], hi, v.z, v.w);
                             }
                         }
+                        xc += NT * 16 * columns;
+                        fetch(q, u + kAhead, w_end - c - kAhead);
                     }
+                    codes0 += kAhead * 64;
+                    codes1 += kAhead * 64;
+                    scales0 += kAhead * 4 * kBlocks;
+                    scales1 += kAhead * 4 * kBlocks;
                 }
             }
+            if (once && round + 1 < rounds)  // the next tile's loads run while this one's sums are added
+                begin(tile_of(round + 1), c_begin, c_end);
             if (mine) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -300,16 +352,17 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                     sums[warp][g + 8][nt * 8 + 2 * t + 1] = acc[nt][3];
                 }
             }
-            // output i of the round: tile i / (16 kPass) of the CTA, row of x, output of the tile
+            // output i of the round: tile slot, row of x, output of the tile
             auto finish = [&](int i, auto &&sum_at) {
                 const int k = i / (kRows * kPass), b = i / kRows % kPass, r = i % kRows;
-                const int j = (tile0 + (k - warp) * clusters + round * hop) * kRows + r;
+                const int j = (cluster + (round * slots + k) * clusters) * kRows + r;
                 if (b0 + b >= rows.y || j >= d_out)
                     return;
                 float sum = 0.f;
 #pragma unroll
                 for (int p = P - 1; p >= 0; --p)  // the small pieces first
-                    sum = sum_at(sum, k, r, b / kTok * 8 + b % kTok * P + p);
+                    for (int q = 0; q < parts; ++q)
+                        sum = sum_at(sum, &sums[k * parts + q][r][b / kTok * 8 + b % kTok * P + p]);
                 sum *= scale;
                 const int64_t o = static_cast<int64_t>(b0 + b) * ldy + j;
                 if (yt == LNQ_BF16)
@@ -319,23 +372,22 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                 else
                     static_cast<float *>(y)[o] = sum;
             };
-            if (shares == 1) {  // a warp has its tile's whole sums
-                __syncwarp();
-                for (int i = lane; i < kRows * kPass; i += 32)
-                    finish(warp * kRows * kPass + i,
-                           [&](float s, int k, int r, int c) { return s + sums[k][r][c]; });
-                __syncwarp();
+            if (shares == 1) {
+                __syncthreads();
+                for (int i = threadIdx.x; i < slots * kRows * kPass; i += kThreads)
+                    finish(i, [](float s, const float *at) { return s + *at; });
+                __syncthreads();
             } else {
                 cluster_sync();
-                for (int i = share * kThreads + threadIdx.x; i < kWarps * kRows * kPass; i += shares * kThreads)
-                    finish(i, [&](float s, int k, int r, int c) {
+                for (int i = share * kThreads + threadIdx.x; i < slots * kRows * kPass; i += shares * kThreads)
+                    finish(i, [&](float s, const float *at) {
                         float v[kMaxShares];
 #pragma unroll
                         for (int q = 0; q < kMaxShares; ++q)
                             if (q < shares)
                                 asm volatile("ld.shared::cluster.f32 %0, [%1];"
                                              : "=f"(v[q])
-                                             : "r"(cluster_addr(&sums[k][r][c], static_cast<uint32_t>(q))));
+                                             : "r"(cluster_addr(at, static_cast<uint32_t>(q))));
 #pragma unroll
                         for (int q = 0; q < kMaxShares; ++q)
                             if (q < shares)
@@ -357,16 +409,7 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
     const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * sizeof(TX) % 16 == 0;
     const int64_t tiles = (w.rows + kRows - 1) / kRows, chunks = (d_in + kChunk - 1) / kChunk;
     const int64_t busy = offsets == nullptr ? 1 : min(experts, static_cast<int64_t>(n));  // experts
-    const int64_t room = 2 * num_sms;  // CTAs that run at once
-    constexpr int kChunkBytes = NT * 128 * 16;
-    // K is shared while there are fewer tiles than warps, or while a share of x does not fit
-    int shares = 1;
-    while (shares < kMaxShares && chunks >= shares * 4 &&
-           (tiles * busy * shares < room * kWarps || chunks * kChunkBytes > static_cast<int64_t>(shares) * kXBytes))
-        shares *= 2;
-    const int panel = static_cast<int>(min((chunks + shares - 1) / shares, static_cast<int64_t>(kXBytes / kChunkBytes)));
-    const int64_t clusters = max(int64_t(1), min((tiles + kWarps - 1) / kWarps,
-                                                 (room + busy * shares - 1) / (busy * shares)));
+    constexpr int64_t kChunkBytes = NT * 128 * 16;
     auto *kernel = fp4_gemv_kernel<TX, FMT, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kXBytes);
     if (e != cudaSuccess)
@@ -374,18 +417,54 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(shares);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * shares), static_cast<unsigned>(experts));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(panel) * kChunkBytes;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    // How K is shared: by `shares` CTAs of a cluster (less of x for each to write) and `parts`
+    // warps of a CTA (fewer idle warps in the last round). The least time, in hundredths of a
+    // tile's chunk (0.65 us measured with two CTAs an SM): a chunk of x staged, a chunk of a tile, and
+    // a round's fixed costs, which are larger where a cluster's CTAs wait for one another.
+    constexpr int64_t kStage = NT * (Pieces<TX>::n == 1 ? 12 : 24), kWork = 80 + 20 * NT;
+    static std::atomic<int> resident[4];  // clusters that run at once, by their size
+    int shares = 1, parts = 1;
+    int64_t clusters = 1, best = INT64_MAX;
+    for (int i = 0, c = 1; c <= kMaxShares && (c == 1 || chunks >= c * 2); ++i, c *= 2) {
+        int room = resident[i].load(std::memory_order_relaxed);
+        if (room == 0) {
+            room = 2 * num_sms / c;
+            if (c > 1) {
+                attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+                cfg.gridDim = dim3(static_cast<unsigned>(room * c));
+                cfg.dynamicSmemBytes = kXBytes;
+                int active = 0;
+                if (cudaOccupancyMaxActiveClusters(&active, kernel, &cfg) == cudaSuccess && active > 0)
+                    room = active;
+                else
+                    (void)cudaGetLastError();  // a failed query is not an error of this call
+            }
+            resident[i].store(room, std::memory_order_relaxed);
+        }
+        const int64_t own = (chunks + c - 1) / c, m = max(int64_t(1), min(tiles, room / busy));
+        const int64_t per_cta = (tiles + m - 1) / m, waves = (m * busy + room - 1) / room;
+        for (int k = 1; k <= kWarps && (k == 1 || own >= k * 2); k *= 2) {
+            const int64_t rounds = (per_cta * k + kWarps - 1) / kWarps;
+            const int64_t stagings = own * kChunkBytes > kXBytes ? rounds : 1;
+            const int64_t cost = waves * (stagings * own * kStage +
+                                          rounds * ((own + k - 1) / k * kWork + (c > 1 ? 500 : 80)));
+            if (cost < best)
+                best = cost, shares = c, parts = k, clusters = m;
+        }
+    }
+    const int64_t panel = min((chunks + shares - 1) / shares, kXBytes / kChunkBytes);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(shares);
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * shares), static_cast<unsigned>(experts));
+    cfg.dynamicSmemBytes = static_cast<size_t>(panel * kChunkBytes);
     KernelTimer timer("lnq_fp4_gemv", s);
     e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const TX *>(x), n, ldx, wide, offsets, w,
-                           static_cast<int>(d_in), y, yt, ldy, shares, panel);
+                           static_cast<int>(d_in), y, yt, ldy, parts, shares, static_cast<int>(panel));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
