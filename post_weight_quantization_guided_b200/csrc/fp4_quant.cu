@@ -3,15 +3,15 @@
 //   MX: s = 2^(floor(log2 amax) - 2) over blocks of 32;  NV: s = E4M3(amax / (6 t)) over 16;
 //   code = E2M1(x / (s t)), nearest, ties to even, at most 6 in magnitude.
 //
-// Bound: HBM (read x, write half a byte an element). One pass: a lane takes 8 consecutive
-// elements (one or two 16-byte loads, 4 bytes of codes out), 4 (MX) or 2 (NV) neighbouring lanes
-// hold a block and agree on its largest element by shuffles, a warp covers 256 elements of a row.
+// Bound: HBM (read x, write half a byte an element). One pass: a lane takes 16 consecutive
+// elements, an NV block or half an MX one (whose two lanes agree on its largest element by a
+// shuffle), a warp 512 elements of a row; two such spans are loaded before the first is worked on.
 //
-// Exact decisions. MX quotients are exact (a power of two). An NV quotient x / (s t) is estimated
-// in 32 bits and rounded to a code twice, a little below and a little above the estimate; where
-// both give one code it is the right one. Where they differ the quotient is near the border b of
-// two codes, and the sign of |x| - (b s) t decides: b s has at most 7 bits, so one fused
-// multiply-add gives that sign exactly. The block scale is found in 64 bits (below).
+// Exact decisions. MX quotients are exact (a power of two). An NV quotient is estimated in 32 bits
+// and rounded twice, a little below and a little above the estimate; where both agree that is the
+// answer. Where they differ the quotient is near the border b of two codes or of two scales. A code
+// is then decided by the sign of |x| - (b s) t: b s has at most 7 bits, so one fused multiply-add
+// gives that sign exactly. A scale is found in 64 bits (below).
 #include <cuda_fp8.h>
 
 #include "fp4.cuh"
@@ -20,53 +20,120 @@
 namespace lnq {
 
 constexpr int kQuantThreads = 256;
-constexpr int kSpan = 256;  // elements of a row that a warp takes at a time (8 a lane)
+constexpr int kLane = 16;          // elements a lane takes at a time
+constexpr int kSpan = 32 * kLane;  // and a warp, of one row
 
 // ------------------------------------------------------------------------------------------
-// Rows of 8 elements
+// A lane's 16 elements
 // ------------------------------------------------------------------------------------------
-// x[0..7], zeros from element `left` on. `wide`: 16-byte loads are possible (and left >= 8).
 template <typename T>
-__device__ __forceinline__ void load8(const T *__restrict__ p, int left, bool wide, float (&v)[8])
-{
-    if (wide && left >= 8) {
-        alignas(16) T e[8];
-        constexpr int kLoads = sizeof(T) * 8 / 16;
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-            reinterpret_cast<uint4 *>(e)[k] = __ldg(reinterpret_cast<const uint4 *>(p) + k);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = to_f32<T>(e[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = k < left ? to_f32<T>(p[k]) : 0.f;
+struct Elements {
+    static constexpr int kWords = kLane * sizeof(T) / 16;
+    uint4 w[kWords];
+    __device__ __forceinline__ T get(int k) const
+    {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(reinterpret_cast<const uint32_t *>(w)[k]);
+        } else {
+            const uint32_t u = reinterpret_cast<const uint32_t *>(w)[k / 2];
+            const unsigned short h = static_cast<unsigned short>(k & 1 ? u >> 16 : u);
+            return *reinterpret_cast<const T *>(&h);
+        }
     }
-}
+    // x[0..15], zeros from element `left` on; `wide`: 16-byte loads are possible
+    __device__ __forceinline__ void load(const T *__restrict__ p, int left, bool wide)
+    {
+        if (wide && left >= kLane) {
+#pragma unroll
+            for (int k = 0; k < kWords; ++k)
+                w[k] = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+            return;
+        }
+        uint32_t *u = reinterpret_cast<uint32_t *>(w);
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                u[k] = k < left ? __float_as_uint(p[k]) : 0u;
+            } else {
+                const uint32_t h = k < left ? reinterpret_cast<const unsigned short *>(p)[k] : 0u;
+                u[k / 2] = k & 1 ? u[k / 2] | (h << 16) : h;
+            }
+        }
+    }
+    // The largest magnitude as the bits of a 32-bit number: above every finite one where there is
+    // a NaN or an infinity.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
+        if constexpr (sizeof(T) == 4) {
+            uint32_t m = u[0] & 0x7FFFFFFFu;
+#pragma unroll
+            for (int k = 1; k < kLane; ++k)
+                m = max(m, u[k] & 0x7FFFFFFFu);
+            return m;
+        } else {
+            uint32_t m = u[0] & 0x7FFF7FFFu;  // 16-bit magnitudes order as whole numbers do
+#pragma unroll
+            for (int k = 1; k < kLane / 2; ++k)
+                m = __vmaxu2(m, u[k] & 0x7FFF7FFFu);
+            const unsigned short h = static_cast<unsigned short>(max(m & 0xFFFFu, m >> 16));
+            return __float_as_uint(to_f32<T>(*reinterpret_cast<const T *>(&h)));
+        }
+    }
+};
 
+// y[0..15] = v for the elements before `left`.
 template <typename T>
-__device__ __forceinline__ void store8(T *__restrict__ p, int left, bool wide, const float (&v)[8])
+__device__ __forceinline__ void store16(T *__restrict__ p, int left, bool wide, const float (&v)[kLane])
 {
-    if (wide && left >= 8) {
-        alignas(16) T e[8];
+    if (wide && left >= kLane) {
+        alignas(16) T e[kLane];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < kLane; ++k)
             e[k] = from_f32<T>(v[k]);
-        constexpr int kStores = sizeof(T) * 8 / 16;
 #pragma unroll
-        for (int k = 0; k < kStores; ++k)
+        for (int k = 0; k < static_cast<int>(kLane * sizeof(T) / 16); ++k)
             reinterpret_cast<uint4 *>(p)[k] = reinterpret_cast<const uint4 *>(e)[k];
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < kLane; ++k)
             if (k < left)
                 p[k] = from_f32<T>(v[k]);
     }
 }
 
+// The spans of a matrix (kSpan elements of a row each), every hop-th for a warp. Rows and spans are
+// carried along: one division a thread, where one a span took a third of the time.
+struct SpanWalk {
+    int64_t row, hop_rows, rows;
+    int span, spans, hop_spans;  // a row has at most 2^24 elements
+    __device__ __forceinline__ SpanWalk(int64_t rows_, int64_t width)
+    {
+        const int64_t warps = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
+        rows = rows_;
+        spans = static_cast<int>((width + kSpan - 1) / kSpan);
+        row = at / spans;
+        span = static_cast<int>(at - row * spans);
+        hop_rows = warps / spans;
+        hop_spans = static_cast<int>(warps - hop_rows * spans);
+    }
+    __device__ __forceinline__ bool more() const { return row < rows; }
+    // this lane's first element of the row
+    __device__ __forceinline__ int element() const { return span * kSpan + (threadIdx.x & 31) * kLane; }
+    __device__ __forceinline__ void next()
+    {
+        row += hop_rows;
+        span += hop_spans;
+        if (span >= spans) {
+            span -= spans;
+            ++row;
+        }
+    }
+};
+
 // The codes of 8 numbers (nearest, ties to even, saturating), element k in bits 4k+3 .. 4k.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8])
+__device__ __forceinline__ uint32_t e2m1x8(const float *q)
 {
     uint32_t out;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -78,6 +145,26 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8])
         : "=r"(out)
         : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
     return out;
+}
+
+// The values of a word's 8 codes.
+__device__ __forceinline__ void code_values(uint32_t w, float *v)
+{
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+    }
 }
 
 // q as a float that rounds to few bits as q itself would: towards zero, and the last bit set if
@@ -93,8 +180,7 @@ __device__ __forceinline__ float to_odd(double q)
 // ------------------------------------------------------------------------------------------
 // What a thread keeps of the matrix scale t.
 struct MatrixScale {
-    float t, rt;       // t, about 1 / t
-    double r6;         // 1 / (6 t)
+    float t, rt, rt6;  // t, about 1 / t, about 1 / (6 t)
     bool valid, fast;  // t positive and finite; s t and 1 / (s t) normal 32-bit numbers for every s
 };
 
@@ -105,7 +191,7 @@ __device__ __forceinline__ MatrixScale matrix_scale(const float *t)
     m.valid = m.t > 0.f && m.t < __uint_as_float(0x7F800000u);
     m.fast = m.t >= 0x1p-100f && m.t <= 0x1p115f;
     m.rt = 1.f / m.t;
-    m.r6 = 1.0 / (6.0 * static_cast<double>(m.t));
+    m.rt6 = m.rt * (1.f / 6.f);
     return m;
 }
 
@@ -113,9 +199,9 @@ __device__ __forceinline__ MatrixScale matrix_scale(const float *t)
 // bits, which puts a quotient on the border of two E4M3 numbers back on it, and moves none that
 // is not there onto it: amax and 6 t b (b a border, 5 bits) are whole numbers of at most 24 and 31
 // bits on one scale, so a quotient off the border is at least 2^-31 away from it.
-__device__ __forceinline__ uint32_t nv_scale_byte(float amax, const MatrixScale &m)
+__device__ __noinline__ uint32_t nv_scale_exact(float amax, float t)
 {
-    const double q = static_cast<double>(amax) * m.r6;
+    const double q = static_cast<double>(amax) / (6.0 * static_cast<double>(t));
     double q40 = q;
     if (q < 1024.0) {
         const double big = __dmul_rn(q, 8193.0);
@@ -124,40 +210,38 @@ __device__ __forceinline__ uint32_t nv_scale_byte(float amax, const MatrixScale 
     return __nv_cvt_float_to_fp8(to_odd(fmin(q40, 1024.0)), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The 8 codes of an NV block with scale s, any t: quotients in 64 bits. A quotient on a border of
-// two codes is exact; any other is at least 2^-31 away from it, further than its rounding.
-__device__ __noinline__ uint32_t nv_codes_slow(const float (&v)[8], float s, float t)
+__device__ __forceinline__ uint32_t nv_scale_byte(float amax, const MatrixScale &m)
 {
-    const double step = static_cast<double>(s) * static_cast<double>(t);
-    float q[8];
-    for (int k = 0; k < 8; ++k)
-        q[k] = to_odd(fmax(-8.0, fmin(8.0, static_cast<double>(v[k]) / step)));
-    return e2m1x8(q);
+    // relative error of amax * rt6 below 2^-21: three roundings and that of the constant
+    const float below = amax * (m.rt6 * (1.f - 0x1p-20f)), above = amax * (m.rt6 * (1.f + 0x1p-20f));
+    unsigned short both;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(both) : "f"(above), "f"(below));
+    const uint32_t byte = both & 255u;
+    return m.fast && byte == (both >> 8) ? byte : nv_scale_exact(amax, m.t);
 }
 
-__device__ __forceinline__ uint32_t nv_codes(const float (&v)[8], float s, const MatrixScale &m)
+// The codes of an NV block's 16 elements with scale s, any t: quotients in 64 bits. A quotient on a
+// border of two codes is exact; any other is at least 2^-31 away from it, further than its rounding.
+__device__ __noinline__ uint2 nv_codes_slow(const float *v, float s, float t)
 {
-    if (!m.fast)
-        return nv_codes_slow(v, s, m.t);
-    // relative error of v * r below 2^-21: three roundings and the approximate reciprocal
-    const float r = __frcp_rn(s) * m.rt;
-    const float below = r * (1.f - 0x1p-20f), above = r * (1.f + 0x1p-20f);
-    float lo[8], hi[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        lo[k] = v[k] * below;
-        hi[k] = v[k] * above;
-    }
-    uint32_t codes = e2m1x8(lo);
-    const uint32_t upper = e2m1x8(hi);
+    const double step = static_cast<double>(s) * static_cast<double>(t);
+    float q[kLane];
+    for (int k = 0; k < kLane; ++k)
+        q[k] = to_odd(fmax(-8.0, fmin(8.0, static_cast<double>(v[k]) / step)));
+    return make_uint2(e2m1x8(q), e2m1x8(q + 8));
+}
+
+// `codes` (of quotients a little too small) where `upper` (a little too large) differs: the border
+// between codes c and c + 1 decides.
+__device__ __forceinline__ uint32_t nv_decide(uint32_t codes, uint32_t upper, const float *v, float s, float t)
+{
     if (codes != upper) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const uint32_t c = (codes >> (4 * k)) & 7u;
             if (((upper >> (4 * k)) & 7u) != c) {
-                // the border between codes c and c + 1
                 const float b = 0.5f * (fp4_code_value(c) + fp4_code_value(c + 1u));
-                const float d = fmaf(-b * s, m.t, fabsf(v[k]));
+                const float d = fmaf(-b * s, t, fabsf(v[k]));
                 if (d > 0.f || (d == 0.f && (c & 1u)))
                     codes += 1u << (4 * k);
             }
@@ -166,64 +250,97 @@ __device__ __forceinline__ uint32_t nv_codes(const float (&v)[8], float s, const
     return codes;
 }
 
+// v[k] * r for pairs, packed.
+__device__ __forceinline__ void scale16(const float (&v)[kLane], float r, float (&q)[kLane])
+{
+    uint64_t rr;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(rr) : "f"(r));
+#pragma unroll
+    for (int k = 0; k < kLane; k += 2) {
+        uint64_t pair;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(pair) : "f"(v[k]), "f"(v[k + 1]));
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(pair) : "l"(rr));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(q[k]), "=f"(q[k + 1]) : "l"(pair));
+    }
+}
+
+__device__ __forceinline__ uint2 nv_codes(const float (&v)[kLane], float s, const MatrixScale &m)
+{
+    if (!m.fast)
+        return nv_codes_slow(v, s, m.t);
+    // relative error of v * r below 2^-21: three roundings and the approximate reciprocal
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r *= m.rt;
+    float lo[kLane], hi[kLane];
+    scale16(v, r * (1.f - 0x1p-20f), lo);
+    scale16(v, r * (1.f + 0x1p-20f), hi);
+    return make_uint2(nv_decide(e2m1x8(lo), e2m1x8(hi), v, s, m.t),
+                      nv_decide(e2m1x8(lo + 8), e2m1x8(hi + 8), v + 8, s, m.t));
+}
+
 // ------------------------------------------------------------------------------------------
 // Kernels
 // ------------------------------------------------------------------------------------------
+constexpr int kSpansAhead = 2;  // spans a warp loads before it works on the first
+
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads)
-    fp4_quantize_kernel(const T *__restrict__ x, int64_t rows, int64_t d, int64_t ldx, bool wide,
+    fp4_quantize_kernel(const T *__restrict__ x, int64_t rows, int d, int64_t ldx, bool wide,
                         const float *__restrict__ t, uint8_t *__restrict__ codes,
                         uint8_t *__restrict__ scales)
 {
-    constexpr int kLanes = fp4_block(FMT) / 8;  // lanes that hold one block
-    const int lane = threadIdx.x & 31;
-    const int64_t padded = fp4_padded(d), spans = (padded + kSpan - 1) / kSpan;
-    const int64_t total = rows * spans;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
+    const int padded = static_cast<int>(fp4_padded(d));
     MatrixScale m;
     if (FMT == LNQ_FP4_NV)
         m = matrix_scale(t);
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
-         w < total; w += stride) {
-        const int64_t row = w / spans;
-        const int64_t i0 = (w - row * spans) * kSpan + lane * 8;
-        const int left = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), d - i0)));
-        float v[8];
-        load8(x + row * ldx + i0, left, wide, v);
-        // largest magnitude, as bits: a NaN or an infinity is above every finite number
-        uint32_t amax = 0u;
+    SpanWalk walk(rows, padded);
+    while (walk.more()) {
+        SpanWalk at[kSpansAhead] = {walk, walk};
+        Elements<T> e[kSpansAhead];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            amax = max(amax, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1)
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        uint32_t byte, word = 0u;
-        if (FMT == LNQ_FP4_MX) {
-            byte = 255u;
-            if (amax < 0x7F800000u) {
-                // exponent field of the scale: that of amax, less 2
-                byte = max(static_cast<int>(amax >> 23) - 2, 0);
-                const float r = __uint_as_float((254u - byte) << 23);
-                float q[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    q[k] = v[k] * r;
-                word = e2m1x8(q);
-            }
-        } else {
-            byte = 127u;
-            if (amax < 0x7F800000u && m.valid) {
-                byte = nv_scale_byte(__uint_as_float(amax), m);
-                if (byte != 0u)
-                    word = nv_codes(v, fp4_scale_value<FMT>(byte), m);
-            }
+        for (int u = 0; u < kSpansAhead; ++u) {
+            at[u] = walk;
+            const int i0 = walk.element();
+            if (walk.more())
+                e[u].load(x + walk.row * ldx + i0, d - i0, wide);
+            walk.next();
         }
-        if (i0 < padded) {
-            reinterpret_cast<uint32_t *>(codes + row * (padded / 2))[i0 / 8] = word;
-            if (lane % kLanes == 0)
-                scales[row * (padded / fp4_block(FMT)) + i0 / fp4_block(FMT)] =
-                    static_cast<uint8_t>(i0 < d ? byte : 0u);
+#pragma unroll
+        for (int u = 0; u < kSpansAhead; ++u) {
+            if (!at[u].more())
+                break;
+            uint32_t amax = e[u].top(), byte;
+            uint2 word = make_uint2(0u, 0u);
+            float v[kLane];
+#pragma unroll
+            for (int k = 0; k < kLane; ++k)
+                v[k] = to_f32<T>(e[u].get(k));
+            if (FMT == LNQ_FP4_MX) {
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                byte = 255u;
+                if (amax < 0x7F800000u) {
+                    // exponent field of the scale: that of amax, less 2
+                    byte = max(static_cast<int>(amax >> 23) - 2, 0);
+                    float q[kLane];
+                    scale16(v, __uint_as_float((254u - byte) << 23), q);
+                    word = make_uint2(e2m1x8(q), e2m1x8(q + 8));
+                }
+            } else {
+                byte = 127u;
+                if (amax < 0x7F800000u && m.valid) {
+                    byte = nv_scale_byte(__uint_as_float(amax), m);
+                    if (byte != 0u)
+                        word = nv_codes(v, __uint_as_float(byte << 20) * 0x1p120f, m);
+                }
+            }
+            const int i0 = at[u].element();
+            if (i0 < padded) {
+                *reinterpret_cast<uint2 *>(codes + at[u].row * (padded / 2) + i0 / 2) = word;
+                if (FMT == LNQ_FP4_NV || (threadIdx.x & 1) == 0)
+                    scales[at[u].row * (padded / fp4_block(FMT)) + i0 / fp4_block(FMT)] =
+                        static_cast<uint8_t>(i0 < d ? byte : 0u);
+            }
         }
     }
 }
@@ -231,29 +348,41 @@ __global__ void __launch_bounds__(kQuantThreads)
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads)
     fp4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                          int64_t rows, int64_t d, const float *__restrict__ t, T *__restrict__ y,
+                          int64_t rows, int d, const float *__restrict__ t, T *__restrict__ y,
                           int64_t ldy, bool wide)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t padded = fp4_padded(d), spans = (padded + kSpan - 1) / kSpan;
-    const int64_t total = rows * spans;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
+    const int padded = static_cast<int>(fp4_padded(d));
     const float tv = t == nullptr ? 1.f : __ldg(t);
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
-         w < total; w += stride) {
-        const int64_t row = w / spans;
-        const int64_t i0 = (w - row * spans) * kSpan + lane * 8;
-        if (i0 >= d)
-            continue;
-        const uint32_t word =
-            __ldg(reinterpret_cast<const uint32_t *>(codes + row * (padded / 2)) + i0 / 8);
-        const float s = fp4_scale_value<FMT>(
-            __ldg(scales + row * (padded / fp4_block(FMT)) + i0 / fp4_block(FMT)));
-        float v[8];
+    SpanWalk walk(rows, padded);
+    while (walk.more()) {
+        SpanWalk at[kSpansAhead] = {walk, walk};
+        uint2 word[kSpansAhead];
+        uint32_t byte[kSpansAhead];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = fp4_code_value((word >> (4 * k)) & 15u) * s * tv;
-        store8(y + row * ldy + i0, static_cast<int>(min(static_cast<int64_t>(8), d - i0)), wide, v);
+        for (int u = 0; u < kSpansAhead; ++u) {
+            at[u] = walk;
+            const int i0 = walk.element();
+            word[u] = make_uint2(0u, 0u);
+            byte[u] = 0u;
+            if (walk.more() && i0 < d) {
+                word[u] = __ldg(reinterpret_cast<const uint2 *>(codes + walk.row * (padded / 2) + i0 / 2));
+                byte[u] = __ldg(scales + walk.row * (padded / fp4_block(FMT)) + i0 / fp4_block(FMT));
+            }
+            walk.next();
+        }
+#pragma unroll
+        for (int u = 0; u < kSpansAhead; ++u) {
+            const int i0 = at[u].element();
+            if (!at[u].more() || i0 >= d)
+                continue;
+            float q[kLane], v[kLane];
+            code_values(word[u].x, q);
+            code_values(word[u].y, q + 8);
+            scale16(q, fp4_scale_value<FMT>(byte[u]), v);
+            if (FMT == LNQ_FP4_NV)
+                scale16(v, tv, v);
+            store16(y + at[u].row * ldy + i0, d - i0, wide, v);
+        }
     }
 }
 
@@ -261,29 +390,37 @@ __global__ void __launch_bounds__(kQuantThreads)
 // order of the blocks does not matter.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads)
-    fp4_absmax_kernel(const T *__restrict__ x, int64_t rows, int64_t d, int64_t ldx, bool wide,
+    fp4_absmax_kernel(const T *__restrict__ x, int64_t rows, int d, int64_t ldx, bool wide,
                       uint32_t *__restrict__ top)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t spans = (d + kSpan - 1) / kSpan, total = rows * spans;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
     uint32_t amax = 0u;
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
-         w < total; w += stride) {
-        const int64_t row = w / spans;
-        const int64_t i0 = (w - row * spans) * kSpan + lane * 8;
-        const int left = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), d - i0)));
-        float v[8];
-        load8(x + row * ldx + i0, left, wide, v);
+    SpanWalk walk(rows, d);
+    while (walk.more()) {
+        Elements<T> e[kSpansAhead];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t b = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-            amax = max(amax, b < 0x7F800000u ? b : 0u);
+        for (int u = 0; u < kSpansAhead; ++u) {
+            const int i0 = walk.element();
+            const bool more = walk.more();
+            e[u].load(x + (more ? walk.row * ldx + i0 : 0), more ? d - i0 : 0, wide);
+            walk.next();
+        }
+#pragma unroll
+        for (int u = 0; u < kSpansAhead; ++u) {
+            uint32_t m = e[u].top();
+            if (m >= 0x7F800000u) {
+                m = 0u;
+#pragma unroll
+                for (int k = 0; k < kLane; ++k) {
+                    const uint32_t b = __float_as_uint(to_f32<T>(e[u].get(k))) & 0x7FFFFFFFu;
+                    m = max(m, b < 0x7F800000u ? b : 0u);
+                }
+            }
+            amax = max(amax, m);
         }
     }
     __shared__ uint32_t part[kQuantThreads / 32];
     amax = __reduce_max_sync(0xffffffffu, amax);
-    if (lane == 0)
+    if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = amax;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -337,7 +474,7 @@ cudaError_t fp4_tensor_scale_launch(const void *x, int xt, int64_t rows, int64_t
         e = by_type(xt, [&](auto *p) {
             using T = std::remove_pointer_t<decltype(p)>;
             fp4_absmax_kernel<T><<<span_blocks(rows, d, num_sms), kQuantThreads, 0, s>>>(
-                static_cast<const T *>(x), rows, d, ldx, wide_rows(x, ldx, sizeof(T)),
+                static_cast<const T *>(x), rows, static_cast<int>(d), ldx, wide_rows(x, ldx, sizeof(T)),
                 reinterpret_cast<uint32_t *>(t));
             return cudaGetLastError();
         });
@@ -358,7 +495,8 @@ cudaError_t fp4_quantize_launch(const void *x, int xt, int64_t rows, int64_t d, 
         auto *kernel = fmt == LNQ_FP4_MX ? fp4_quantize_kernel<T, LNQ_FP4_MX>
                                          : fp4_quantize_kernel<T, LNQ_FP4_NV>;
         kernel<<<span_blocks(rows, d, num_sms), kQuantThreads, 0, s>>>(
-            static_cast<const T *>(x), rows, d, ldx, wide_rows(x, ldx, sizeof(T)), t, codes, scales);
+            static_cast<const T *>(x), rows, static_cast<int>(d), ldx, wide_rows(x, ldx, sizeof(T)), t,
+            codes, scales);
         return cudaGetLastError();
     });
 }
@@ -373,7 +511,8 @@ cudaError_t fp4_dequantize_launch(const uint8_t *codes, const uint8_t *scales, i
         auto *kernel = fmt == LNQ_FP4_MX ? fp4_dequantize_kernel<T, LNQ_FP4_MX>
                                          : fp4_dequantize_kernel<T, LNQ_FP4_NV>;
         kernel<<<span_blocks(rows, d, num_sms), kQuantThreads, 0, s>>>(
-            codes, scales, rows, d, t, static_cast<T *>(y), ldy, wide_rows(y, ldy, sizeof(T)));
+            codes, scales, rows, static_cast<int>(d), t, static_cast<T *>(y), ldy,
+            wide_rows(y, ldy, sizeof(T)));
         return cudaGetLastError();
     });
 }
