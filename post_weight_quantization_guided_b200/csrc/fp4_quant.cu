@@ -82,26 +82,6 @@ struct Elements {
     }
 };
 
-// y[0..15] = v for the elements before `left`.
-template <typename T>
-__device__ __forceinline__ void store16(T *__restrict__ p, int left, bool wide, const float (&v)[kLane])
-{
-    if (wide && left >= kLane) {
-        alignas(16) T e[kLane];
-#pragma unroll
-        for (int k = 0; k < kLane; ++k)
-            e[k] = from_f32<T>(v[k]);
-#pragma unroll
-        for (int k = 0; k < static_cast<int>(kLane * sizeof(T) / 16); ++k)
-            reinterpret_cast<uint4 *>(p)[k] = reinterpret_cast<const uint4 *>(e)[k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < kLane; ++k)
-            if (k < left)
-                p[k] = from_f32<T>(v[k]);
-    }
-}
-
 // The spans of a matrix (kSpan elements of a row each), every hop-th for a warp. Rows and spans are
 // carried along: one division a thread, where one a span took a third of the time.
 struct SpanWalk {
@@ -147,7 +127,8 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *q)
     return out;
 }
 
-// The values of a word's 8 codes.
+// The values of a word's 8 codes. (All are used: with four of them unused the compiler was seen to
+// give zeros for the others.)
 __device__ __forceinline__ void code_values(uint32_t w, float *v)
 {
     uint32_t h[4];
@@ -345,43 +326,56 @@ __global__ void __launch_bounds__(kQuantThreads)
     }
 }
 
+// A lane writes 16 bytes at a time, its neighbours the next, so that a warp's store is 512 bytes in
+// a row (two stores of alternate 16-byte pieces were a quarter slower).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads)
     fp4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                           int64_t rows, int d, const float *__restrict__ t, T *__restrict__ y,
                           int64_t ldy, bool wide)
 {
+    constexpr int kPiece = 16 / sizeof(T), kPieces = kSpan / 32 / kPiece;
     const int padded = static_cast<int>(fp4_padded(d));
+    const int lane = threadIdx.x & 31;
     const float tv = t == nullptr ? 1.f : __ldg(t);
-    SpanWalk walk(rows, padded);
-    while (walk.more()) {
-        SpanWalk at[kSpansAhead] = {walk, walk};
-        uint2 word[kSpansAhead];
-        uint32_t byte[kSpansAhead];
+    for (SpanWalk walk(rows, padded); walk.more(); walk.next()) {
+        const uint8_t *c = codes + walk.row * (padded / 2), *s = scales + walk.row * (padded / fp4_block(FMT));
+        T *out = y + walk.row * ldy;
+        const int i0 = walk.span * kSpan + lane * kPiece;
+        uint32_t word[kPieces], byte[kPieces];
 #pragma unroll
-        for (int u = 0; u < kSpansAhead; ++u) {
-            at[u] = walk;
-            const int i0 = walk.element();
-            word[u] = make_uint2(0u, 0u);
-            byte[u] = 0u;
-            if (walk.more() && i0 < d) {
-                word[u] = __ldg(reinterpret_cast<const uint2 *>(codes + walk.row * (padded / 2) + i0 / 2));
-                byte[u] = __ldg(scales + walk.row * (padded / fp4_block(FMT)) + i0 / fp4_block(FMT));
+        for (int p = 0; p < kPieces; ++p) {
+            const int i = i0 + p * 32 * kPiece;
+            word[p] = byte[p] = 0u;
+            if (i < d) {
+                word[p] = __ldg(reinterpret_cast<const uint32_t *>(c) + i / 8) >> (4 * (i & 4));
+                byte[p] = __ldg(s + i / fp4_block(FMT));
             }
-            walk.next();
         }
 #pragma unroll
-        for (int u = 0; u < kSpansAhead; ++u) {
-            const int i0 = at[u].element();
-            if (!at[u].more() || i0 >= d)
-                continue;
-            float q[kLane], v[kLane];
-            code_values(word[u].x, q);
-            code_values(word[u].y, q + 8);
-            scale16(q, fp4_scale_value<FMT>(byte[u]), v);
-            if (FMT == LNQ_FP4_NV)
-                scale16(v, tv, v);
-            store16(y + at[u].row * ldy + i0, d - i0, wide, v);
+        for (int p = 0; p < kPieces; ++p) {
+            const int i = i0 + p * 32 * kPiece;
+            const float scale = fp4_scale_value<FMT>(byte[p]);
+            float v[8];
+            if constexpr (kPiece == 8) {
+                code_values(word[p], v);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kPiece; ++k)
+                    v[k] = fp4_code_value((word[p] >> (4 * k)) & 15u);
+            }
+            alignas(16) T e[kPiece];
+#pragma unroll
+            for (int k = 0; k < kPiece; ++k)
+                e[k] = from_f32<T>(v[k] * scale * tv);
+            if (wide && i + kPiece <= d) {
+                *reinterpret_cast<uint4 *>(out + i) = *reinterpret_cast<const uint4 *>(e);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kPiece; ++k)
+                    if (i + k < d)
+                        out[i + k] = e[k];
+            }
         }
     }
 }
