@@ -5,14 +5,18 @@
 //
 // Bound: HBM (read x, write half a byte an element). One pass: a lane takes 16 consecutive
 // elements, an NV block or half an MX one (whose two lanes agree on its largest element by a
-// shuffle), a warp 512 elements of a row; two such spans are loaded before the first is worked on.
+// shuffle), a warp 512 elements of a row. NV is bound by its two roundings instead (61 us for
+// 16384 x 4096 bf16, where MX takes 35 and its bytes 26).
 //
 // Exact decisions. MX quotients are exact (a power of two). An NV quotient is estimated in 32 bits
 // and rounded twice, a little below and a little above the estimate; where both agree that is the
-// answer. Where they differ the quotient is near the border b of two codes or of two scales. A code
-// is then decided by the sign of |x| - (b s) t: b s has at most 7 bits, so one fused multiply-add
-// gives that sign exactly. A scale is found in 64 bits (below).
+// answer. Where they differ the quotient is near the border b of two codes or of two scales (ties
+// are frequent: 16-bit elements over a t that comes from one of them). A code is then decided by the
+// sign of |x| - (b s) t: b s has at most 7 bits, so one fused multiply-add gives that sign exactly.
+// A scale is found in 64 bits (below).
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "profile.cuh"
@@ -72,10 +76,16 @@ struct Elements {
                 m = max(m, u[k] & 0x7FFFFFFFu);
             return m;
         } else {
-            uint32_t m = u[0] & 0x7FFF7FFFu;  // 16-bit magnitudes order as whole numbers do
+            // pairs; the maximum with a NaN is a NaN, whose bits are above an infinity's
+            uint32_t m = u[0] & 0x7FFF7FFFu;
 #pragma unroll
-            for (int k = 1; k < kLane / 2; ++k)
-                m = __vmaxu2(m, u[k] & 0x7FFF7FFFu);
+            for (int k = 1; k < kLane / 2; ++k) {
+                const uint32_t a = u[k] & 0x7FFF7FFFu;
+                if constexpr (std::is_same_v<T, __nv_bfloat16>)
+                    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(a));
+                else
+                    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(a));
+            }
             const unsigned short h = static_cast<unsigned short>(max(m & 0xFFFFu, m >> 16));
             return __float_as_uint(to_f32<T>(*reinterpret_cast<const T *>(&h)));
         }
@@ -212,25 +222,6 @@ __device__ __noinline__ uint2 nv_codes_slow(const float *v, float s, float t)
     return make_uint2(e2m1x8(q), e2m1x8(q + 8));
 }
 
-// `codes` (of quotients a little too small) where `upper` (a little too large) differs: the border
-// between codes c and c + 1 decides.
-__device__ __forceinline__ uint32_t nv_decide(uint32_t codes, uint32_t upper, const float *v, float s, float t)
-{
-    if (codes != upper) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t c = (codes >> (4 * k)) & 7u;
-            if (((upper >> (4 * k)) & 7u) != c) {
-                const float b = 0.5f * (fp4_code_value(c) + fp4_code_value(c + 1u));
-                const float d = fmaf(-b * s, t, fabsf(v[k]));
-                if (d > 0.f || (d == 0.f && (c & 1u)))
-                    codes += 1u << (4 * k);
-            }
-        }
-    }
-    return codes;
-}
-
 // v[k] * r for pairs, packed.
 __device__ __forceinline__ void scale16(const float (&v)[kLane], float r, float (&q)[kLane])
 {
@@ -253,18 +244,32 @@ __device__ __forceinline__ uint2 nv_codes(const float (&v)[kLane], float s, cons
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     r *= m.rt;
-    float lo[kLane], hi[kLane];
-    scale16(v, r * (1.f - 0x1p-20f), lo);
-    scale16(v, r * (1.f + 0x1p-20f), hi);
-    return make_uint2(nv_decide(e2m1x8(lo), e2m1x8(hi), v, s, m.t),
-                      nv_decide(e2m1x8(lo + 8), e2m1x8(hi + 8), v + 8, s, m.t));
+    float q[kLane];
+    scale16(v, r * (1.f - 0x1p-20f), q);
+    const uint2 below = make_uint2(e2m1x8(q), e2m1x8(q + 8));
+    scale16(v, r * (1.f + 0x1p-20f), q);
+    const uint2 above = make_uint2(e2m1x8(q), e2m1x8(q + 8));
+    if (below.x != above.x || below.y != above.y) {
+        // Some quotient is near a border. A border has three significant bits, so the one near a
+        // quotient is the quotient rounded to three; the sign of |v| - (b s) t is exact. A quotient
+        // off the border is moved away from it, to that side, by more than its error and less than
+        // the way to any other; one that is on it becomes the border, a tie.
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) {
+            const float e = v[k] * r;
+            const float b = __uint_as_float((__float_as_uint(e) + 0x00100000u) & 0xFFE00000u);
+            const float d = fmaf(-b * s, m.t, v[k]);
+            const uint32_t sign = (__float_as_uint(d) ^ __float_as_uint(v[k])) & 0x80000000u;
+            q[k] = d == 0.f ? b : e * (1.f + __uint_as_float(sign | 0x36000000u));  // 2^-19
+        }
+        return make_uint2(e2m1x8(q), e2m1x8(q + 8));
+    }
+    return below;
 }
 
 // ------------------------------------------------------------------------------------------
 // Kernels
 // ------------------------------------------------------------------------------------------
-constexpr int kSpansAhead = 2;  // spans a warp loads before it works on the first
-
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads)
     fp4_quantize_kernel(const T *__restrict__ x, int64_t rows, int d, int64_t ldx, bool wide,
@@ -275,53 +280,39 @@ __global__ void __launch_bounds__(kQuantThreads)
     MatrixScale m;
     if (FMT == LNQ_FP4_NV)
         m = matrix_scale(t);
-    SpanWalk walk(rows, padded);
-    while (walk.more()) {
-        SpanWalk at[kSpansAhead] = {walk, walk};
-        Elements<T> e[kSpansAhead];
+    for (SpanWalk walk(rows, padded); walk.more(); walk.next()) {
+        const int i0 = walk.element();
+        Elements<T> e;
+        e.load(x + walk.row * ldx + i0, d - i0, wide);
+        uint32_t amax = e.top(), byte;
+        uint2 word = make_uint2(0u, 0u);
+        float v[kLane];
 #pragma unroll
-        for (int u = 0; u < kSpansAhead; ++u) {
-            at[u] = walk;
-            const int i0 = walk.element();
-            if (walk.more())
-                e[u].load(x + walk.row * ldx + i0, d - i0, wide);
-            walk.next();
+        for (int k = 0; k < kLane; ++k)
+            v[k] = to_f32<T>(e.get(k));
+        if (FMT == LNQ_FP4_MX) {
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            byte = 255u;
+            if (amax < 0x7F800000u) {
+                // exponent field of the scale: that of amax, less 2
+                byte = max(static_cast<int>(amax >> 23) - 2, 0);
+                float q[kLane];
+                scale16(v, __uint_as_float((254u - byte) << 23), q);
+                word = make_uint2(e2m1x8(q), e2m1x8(q + 8));
+            }
+        } else {
+            byte = 127u;
+            if (amax < 0x7F800000u && m.valid) {
+                byte = nv_scale_byte(__uint_as_float(amax), m);
+                if (byte != 0u)
+                    word = nv_codes(v, __uint_as_float(byte << 20) * 0x1p120f, m);
+            }
         }
-#pragma unroll
-        for (int u = 0; u < kSpansAhead; ++u) {
-            if (!at[u].more())
-                break;
-            uint32_t amax = e[u].top(), byte;
-            uint2 word = make_uint2(0u, 0u);
-            float v[kLane];
-#pragma unroll
-            for (int k = 0; k < kLane; ++k)
-                v[k] = to_f32<T>(e[u].get(k));
-            if (FMT == LNQ_FP4_MX) {
-                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                byte = 255u;
-                if (amax < 0x7F800000u) {
-                    // exponent field of the scale: that of amax, less 2
-                    byte = max(static_cast<int>(amax >> 23) - 2, 0);
-                    float q[kLane];
-                    scale16(v, __uint_as_float((254u - byte) << 23), q);
-                    word = make_uint2(e2m1x8(q), e2m1x8(q + 8));
-                }
-            } else {
-                byte = 127u;
-                if (amax < 0x7F800000u && m.valid) {
-                    byte = nv_scale_byte(__uint_as_float(amax), m);
-                    if (byte != 0u)
-                        word = nv_codes(v, __uint_as_float(byte << 20) * 0x1p120f, m);
-                }
-            }
-            const int i0 = at[u].element();
-            if (i0 < padded) {
-                *reinterpret_cast<uint2 *>(codes + at[u].row * (padded / 2) + i0 / 2) = word;
-                if (FMT == LNQ_FP4_NV || (threadIdx.x & 1) == 0)
-                    scales[at[u].row * (padded / fp4_block(FMT)) + i0 / fp4_block(FMT)] =
-                        static_cast<uint8_t>(i0 < d ? byte : 0u);
-            }
+        if (i0 < padded) {
+            *reinterpret_cast<uint2 *>(codes + walk.row * (padded / 2) + i0 / 2) = word;
+            if (FMT == LNQ_FP4_NV || (threadIdx.x & 1) == 0)
+                scales[walk.row * (padded / fp4_block(FMT)) + i0 / fp4_block(FMT)] =
+                    static_cast<uint8_t>(i0 < d ? byte : 0u);
         }
     }
 }
@@ -387,6 +378,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     fp4_absmax_kernel(const T *__restrict__ x, int64_t rows, int d, int64_t ldx, bool wide,
                       uint32_t *__restrict__ top)
 {
+    constexpr int kSpansAhead = 2;  // loaded before the first is worked on
     uint32_t amax = 0u;
     SpanWalk walk(rows, d);
     while (walk.more()) {

@@ -7,7 +7,6 @@ holds their tensors whichever device is current.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -64,30 +63,33 @@ def lnq_fp4_scale_bytes(d: int, fmt: int) -> int:
 
 def _need(t, dtype, shape, name, device):
     """A contiguous CUDA tensor of this type and shape, on `device`."""
-    if (t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous()
-            or t.device != device):
+    if t.dtype != dtype or t.shape != shape or t.device != device or not device.type == "cuda" \
+            or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _dense(t, name, shape=None, device=None) -> Tuple[int, int]:
     """(type selector, row pitch) of an unquantised matrix [rows][d]; its rows may be strided."""
-    if (t.dim() != 2 or t.dtype not in _DTYPE or not t.is_cuda or t.shape[1] < 1
-            or (shape is not None and t.shape != shape)
-            or (device is not None and t.device != device)):
+    kind, got = _DTYPE.get(t.dtype), t.shape
+    if (kind is None or len(got) != 2 or got[1] < 1 or not t.is_cuda
+            or (shape is not None and (got != shape or t.device != device))):
         raise ValueError(f"{name}: expected a CUDA float32, bfloat16 or float16 matrix"
                          f"{'' if shape is None else f' {tuple(shape)} on {device}'}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, d = t.shape
-    pitch = t.stride(0) if rows > 1 else d
-    if pitch < d or (d > 1 and t.stride(1) != 1):
+    rows, d = got
+    if t.is_contiguous():
+        return kind, d
+    pitch, step = t.stride()
+    pitch = pitch if rows > 1 else d
+    if pitch < d or (d > 1 and step != 1):
         raise ValueError(f"{name}: expected rows of consecutive elements that do not overlap, got "
                          f"strides {t.stride()}")
-    return _DTYPE[t.dtype], pitch
+    return kind, pitch
 
 
 def _format(fmt) -> int:
-    if fmt not in (LNQ_FP4_MX, LNQ_FP4_NV):
+    if fmt != LNQ_FP4_MX and fmt != LNQ_FP4_NV:
         raise ValueError(f"fmt: expected LNQ_FP4_MX or LNQ_FP4_NV, got {fmt!r}")
     return int(fmt)
 
@@ -98,12 +100,17 @@ def _out_type(dtype):
     return dtype
 
 
+def _pitches(d, fmt) -> Tuple[int, int]:
+    """Bytes per row of codes and of scales."""
+    pad = -(-d // 128)
+    return pad * 64, pad * (4 if fmt == LNQ_FP4_MX else 8)
+
+
 def _codes(codes, scales, d, fmt, name, device, lead):
     """Checks the stored form of matrices [*lead][d]."""
-    pad = -(-d // 128)
-    _need(codes, torch.uint8, (*lead, pad * 64), f"{name} codes", device)
-    _need(scales, torch.uint8, (*lead, pad * (4 if fmt == LNQ_FP4_MX else 8)), f"{name} scales",
-          device)
+    of_codes, of_scales = _pitches(d, fmt)
+    _need(codes, torch.uint8, (*lead, of_codes), f"{name} codes", device)
+    _need(scales, torch.uint8, (*lead, of_scales), f"{name} scales", device)
 
 
 def _scale(t, count, fmt, name, device):
@@ -112,23 +119,40 @@ def _scale(t, count, fmt, name, device):
         return None
     if fmt == LNQ_FP4_MX:
         raise ValueError(f"{name}: LNQ_FP4_MX has no matrix scale")
-    if t.dtype != torch.float32 or t.numel() != count or not t.is_cuda or t.device != device \
+    if t.dtype != torch.float32 or t.numel() != count or t.device != device \
             or not t.is_contiguous():
         raise ValueError(f"{name}: expected {count} contiguous CUDA float32 on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
+def _empty(like, shape, dtype):
+    """An uninitialised tensor on the device of `like`."""
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _output(y, like, shape, dtype):
+    """(y, its type selector, its row pitch): the y given, or a new one of `dtype`."""
+    if y is None:
+        return _empty(like, shape, _out_type(dtype)), _DTYPE[dtype], shape[1]
+    return y, *_dense(y, "y", shape, like.device)
+
+
 def _call(name, device, stream, *args):
     """Calls the entry point with the tensors' device current, on `stream` or that device's
     current stream."""
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device != device:
         raise ValueError(f"{name}: the stream is of {stream.device}, the tensors are on {device}")
-    with contextlib.nullcontext() if torch.cuda.current_device() == device.index \
-            else torch.cuda.device(device):
-        status = getattr(lib(), name)(*args, stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = getattr(lib(), name)(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib(), name)(*args, handle)
     if status:
         raise LnqError(status, name)
 
@@ -138,7 +162,7 @@ def lnq_fp4_tensor_scale(x: torch.Tensor, t: Optional[torch.Tensor] = None,
     """t [1]: the matrix scale of LNQ_FP4_NV for x [rows][d], the largest finite |x| / 2688."""
     xt, ldx = _dense(x, "x")
     if t is None:
-        t = torch.empty(1, dtype=torch.float32, device=x.device)
+        t = _empty(x, (1,), torch.float32)
     _need(t, torch.float32, (1,), "t", x.device)
     _call("lnq_fp4_tensor_scale", x.device, stream, x.data_ptr(), xt, x.shape[0], x.shape[1], ldx,
           t.data_ptr())
@@ -153,13 +177,15 @@ def lnq_fp4_quantize(x: torch.Tensor, fmt: int, tensor_scale: Optional[torch.Ten
     xt, ldx = _dense(x, "x")
     fmt, (rows, d), dev = _format(fmt), x.shape, x.device
     ts = _scale(tensor_scale, 1, fmt, "tensor_scale", dev)
-    pad = -(-d // 128)
+    of_codes, of_scales = _pitches(d, fmt)
     if codes is None:
-        codes = torch.empty((rows, pad * 64), dtype=torch.uint8, device=dev)
+        codes = _empty(x, (rows, of_codes), torch.uint8)
+    else:
+        _need(codes, torch.uint8, (rows, of_codes), "codes", dev)
     if scales is None:
-        scales = torch.empty((rows, pad * (4 if fmt == LNQ_FP4_MX else 8)), dtype=torch.uint8,
-                             device=dev)
-    _codes(codes, scales, d, fmt, "output", dev, (rows,))
+        scales = _empty(x, (rows, of_scales), torch.uint8)
+    else:
+        _need(scales, torch.uint8, (rows, of_scales), "scales", dev)
     _call("lnq_fp4_quantize", dev, stream, x.data_ptr(), xt, rows, d, ldx, fmt, ts,
           codes.data_ptr(), scales.data_ptr())
     return codes, scales
@@ -174,9 +200,7 @@ def lnq_fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int, fmt: i
     rows = codes.shape[0]
     _codes(codes, scales, d, fmt, "input", dev, (rows,))
     ts = _scale(tensor_scale, 1, fmt, "tensor_scale", dev)
-    if y is None:
-        y = torch.empty((rows, d), dtype=_out_type(dtype), device=dev)
-    yt, ldy = _dense(y, "y", (rows, d), dev)
+    y, yt, ldy = _output(y, codes, (rows, d), dtype)
     _call("lnq_fp4_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, d, fmt, ts,
           y.data_ptr(), yt, ldy)
     return y
@@ -200,9 +224,7 @@ def _gemv(name, x, offsets, codes, scales, fmt, tensor_scale, y, dtype, stream):
     ts = _scale(tensor_scale, lead[0] if grouped else 1, fmt, "tensor_scale", dev)
     if grouped:
         _offsets(offsets, lead[0], dev)
-    if y is None:
-        y = torch.empty((n, lead[-1]), dtype=_out_type(dtype or x.dtype), device=dev)
-    yt, ldy = _dense(y, "y", (n, lead[-1]), dev)
+    y, yt, ldy = _output(y, codes, (n, lead[-1]), dtype or x.dtype)
     group = (offsets.data_ptr(), lead[0]) if grouped else ()
     _call(name, dev, stream, x.data_ptr(), xt, n, ldx, *group, codes.data_ptr(),
           scales.data_ptr(), ts, lead[-1], d_in, fmt, y.data_ptr(), yt, ldy)
@@ -245,9 +267,7 @@ def _gemm(name, a_codes, a_scales, offsets, codes, scales, d_in, fmt, a_scale, b
     tb = _scale(b_scale, lead[0] if grouped else 1, fmt, "b_scale", dev)
     if grouped:
         _offsets(offsets, lead[0], dev)
-    if y is None:
-        y = torch.empty((n, lead[-1]), dtype=_out_type(dtype), device=dev)
-    yt, ldy = _dense(y, "y", (n, lead[-1]), dev)
+    y, yt, ldy = _output(y, codes, (n, lead[-1]), dtype)
     group = (offsets.data_ptr(), lead[0]) if grouped else ()
     _call(name, dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), ta, n, *group,
           codes.data_ptr(), scales.data_ptr(), tb, lead[-1], d_in, fmt, y.data_ptr(), yt, ldy)
