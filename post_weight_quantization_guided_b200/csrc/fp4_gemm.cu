@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < kScaleRing; ++s) {
-            mbar_init(&sf_raw[s], p.sf_tma ? 1 : 32);
+            mbar_init(&sf_raw[s], 1);
             mbar_init(&sf_ready[s], 2);
             mbar_init(&sf_empty[s], 1);
         }
@@ -311,84 +311,88 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 }
             }
         }
-    } else if (warp == kLoadWarp && !p.sf_tma) {
+    } else if ((warp == kScaleWarp || warp == kLoadWarp) && !p.sf_tma) {
         // ------------------------------------------------------------------ scales without TMA
-        // Rows that are no multiples of 16 bytes: loads of half a stage's bytes, one step
-        // ahead of their stores, in registers.
-        uint32_t v[kGroups * 4][2 * W];
-        int64_t next_tile = first;
-        int next_kb = kb0;
-        Fp4TileAt at = {0, 0, 0, 0};
-        if (next_tile < num_tiles)
-            at = tile_at<BN>(next_tile, p, lim, pre);
-        auto fetch = [&]() {
-            if (next_tile >= num_tiles)
-                return;
-#pragma unroll
-            for (int g = 0; g < kGroups * 4; ++g) {
-                // rows outside the arrays (nobody reads their sums) repeat the last one
-                const int64_t row = g < 4 ? static_cast<int64_t>(at.e) * p.d_out + at.j0 +
-                                                static_cast<int>(cr) * BM + g * 32 + lane
-                                          : static_cast<int64_t>(at.b0) + (g - 4) * 32 + lane;
-                const int64_t top = (g < 4 ? p.w_total : static_cast<int64_t>(p.n)) - 1;
-                const uint8_t *src = (g < 4 ? p.w_scales : p.a_scales) + min(row, top) * p.scale_pitch;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int o = next_kb * 4 * W + u * 2 * W;
-#pragma unroll
-                    for (int k = 0; k < W / 2; ++k)
-                        v[g][u * (W / 2) + k] = 0u;
-                    if (o < p.scale_pitch && (g - 4) * 32 < BN)
-                        ldg_words<W / 2>(v[g] + u * (W / 2), src + o);
-                }
+        // Rows that are no multiples of 16 bytes. The two warps take steps in turn: loads of half a
+        // stage's bytes, four lanes to a row's step and eight rows at a time, into registers
+        // while the step before is in use; then each word to its place in its atom.
+        constexpr int kSets = kGroups * 16, N = W / 2;  // N: words a lane loads of a row
+        const uint32_t ready_leader = cluster_addr(&sf_ready[0], leader);
+        const int unit = lane & 3, r = lane >> 2;
+        uint32_t v[kSets][N];
+        int64_t tile = first;
+        int kb = kb0, slot = 0;
+        uint32_t phase = 1u;
+        auto advance = [&]() {
+            kb += 2;
+            if (kb >= kb1) {
+                kb = kb0;
+                tile += step;
             }
-            next_kb += 2;
-            if (next_kb >= kb1) {
-                next_kb = kb0;
-                next_tile += step;
-                if (next_tile < num_tiles)
-                    at = tile_at<BN>(next_tile, p, lim, pre);
+            slot = slot + 1 == kScaleRing ? 0 : slot + 1;
+            phase ^= slot == 0 ? 1u : 0u;
+        };
+        auto fetch = [&]() {
+            if (tile >= num_tiles)
+                return;
+            const Fp4TileAt at = tile_at<BN>(tile, p, lim, pre);
+            // rows outside the arrays (nobody reads their sums) repeat the last one
+            const int64_t w0 = min(static_cast<int64_t>(at.e) * p.d_out + at.j0 + static_cast<int>(cr) * BM,
+                                   p.w_total - 1);
+            const int wtop = static_cast<int>(min(p.w_total - 1 - w0, static_cast<int64_t>(BM)));
+            const int atop = min(p.n - 1 - at.b0, BN), o = (kb * W + unit * N) * 4;
+            const uint8_t *wsrc = p.w_scales + w0 * p.scale_pitch + o;
+            const uint8_t *asrc = p.a_scales + static_cast<int64_t>(at.b0) * p.scale_pitch + o;
+#pragma unroll
+            for (int g = 0; g < kSets; ++g) {
+                const int row = g < 16 ? min(g * 8 + r, wtop) : min((g - 16) * 8 + r, atop);
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    v[g][k] = 0u;
+                if (o < p.scale_pitch && (g - 16) * 8 < BN)
+                    ldg_words<N>(v[g], (g < 16 ? wsrc : asrc) + static_cast<int64_t>(row) * p.scale_pitch);
             }
         };
+        if (warp == kLoadWarp)
+            advance();
         fetch();
-        int slot = 0;
-        uint32_t phase = 1u;
-        bool ok = true;
-        for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
-            for (int kb = kb0; kb < kb1; kb += 2) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase, p.limit))) {
-                    if (lane == 0)
-                        raise_error(err, kErrTimeout, 2);
-                    ok = false;
-                    break;
-                }
-                const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
-#pragma unroll
-                for (int g = 0; g < kGroups * 4; ++g) {
-                    if ((g - 4) * 32 >= BN)
-                        continue;
-                    uint32_t *w = v[g];
-#pragma unroll
-                    for (int k = 0; k < 2 * W; ++k)  // nothing behind the row's last block
-                        w[k] &= first_bytes(p.blocks - kb * 4 * W - 4 * k);
-#pragma unroll
-                    for (int c = 0; c < W / 2; ++c)
-                        sts_words4(st + T::chunk_at(g * 32 + lane, c), w[4 * c], w[4 * c + 1],
-                                   w[4 * c + 2], w[4 * c + 3]);
-                }
-                mbar_arrive(&sf_raw[slot]);
-                fetch();
-                slot = slot + 1 == kScaleRing ? 0 : slot + 1;
-                phase ^= slot == 0 ? 1u : 0u;
+        while (tile < num_tiles) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase, p.limit))) {
+                if (lane == 0)
+                    raise_error(err, kErrTimeout, 2);
+                break;
             }
+            const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
+#pragma unroll
+            for (int g = 0; g < kSets; ++g) {
+                if ((g - 16) * 8 >= BN)
+                    continue;
+                const int i = g % 16 * 8 + r, group = g / 16;  // row of its 128
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int word = unit * N + k;  // of the row's step
+                    const int h = word / W, a = word % W;
+                    const int atom = h * W * kGroups + (group == 0 ? a : W + a * T::kAtomsN + group - 1);
+                    // nothing behind the row's last block
+                    sts_word(st + static_cast<uint32_t>(atom * kAtom + (i & 31) * 16 + (i >> 5) * 4),
+                             v[g][k] & first_bytes(p.blocks - (kb * W + word) * 4));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_remote(ready_leader + static_cast<uint32_t>(slot * 8));
+            advance();
+            advance();
+            fetch();
         }
     } else if (warp == kScaleWarp || warp == kLoadWarp) {
         // ------------------------------------------------------------------ scales into atoms
         // Lane l takes rows l, l + 32, l + 64, l + 96 of each 128 and writes, for each word of
         // the rows, the four rows' words as 16 bytes of the word's atom: in place, so everything is
-        // read before anything is written. Two warps take turns where TMA loads the scales.
+        // read before anything is written. The two warps take steps in turn.
         const uint32_t ready_leader = cluster_addr(&sf_ready[0], leader);
-        const int turns = p.sf_tma ? 2 : 1, my_turn = warp == kScaleWarp ? 0 : 1;
+        const int my_turn = warp == kScaleWarp ? 0 : 1;
         int slot = 0, turn = 0;
         uint32_t phase = 0u;
         bool ok = true;
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 const bool mine = turn == my_turn;
                 slot = slot + 1 == kScaleRing ? 0 : slot + 1;
                 phase ^= slot == 0 ? 1u : 0u;
-                turn = turn + 1 == turns ? 0 : turn + 1;
+                turn ^= 1;
                 if (!mine)
                     continue;
                 if (!__all_sync(0xffffffffu, mbar_wait(&sf_raw[at_slot], at_phase, p.limit))) {

@@ -47,6 +47,10 @@ __device__ __forceinline__ void ldg_words(uint32_t *v, const uint8_t *src)
         v[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
     }
 }
+__device__ __forceinline__ void sts_word(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Four consecutive words of shared memory.
 __device__ __forceinline__ void lds_words4(uint32_t *v, uint32_t addr)
 {
