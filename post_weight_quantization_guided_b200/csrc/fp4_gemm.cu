@@ -587,25 +587,34 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
 #pragma unroll
         for (int s = 0; s < kMaxSplit; ++s)
             peer[s] = cluster_addr(smem, 2u * (s < p.split ? s : 0) + cr);
-        for (int i = r0 * BM + static_cast<int>(threadIdx.x); i < r1 * BM; i += kThreads) {
-            float sum = 0.f;
+        // four consecutive outputs a thread
+        for (int i = r0 * (BM / 4) + static_cast<int>(threadIdx.x); i < r1 * (BM / 4); i += kThreads) {
+            float u[kMaxSplit][4];
 #pragma unroll
             for (int s = 0; s < kMaxSplit; ++s)
-                if (s < p.split) {
-                    float u;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(peer[s] + i * 4));
-                    sum = s == 0 ? u : sum + u;
-                }
-            const int j = at.j0 + static_cast<int>(cr) * BM + i % BM;
-            if (j < p.d_out) {
-                const int64_t o = static_cast<int64_t>(at.b0 + i / BM) * p.ldy + j;
+                if (s < p.split)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(u[s][0]), "=f"(u[s][1]), "=f"(u[s][2]), "=f"(u[s][3])
+                                 : "r"(peer[s] + i * 16)
+                                 : "memory");
+            const int j = at.j0 + static_cast<int>(cr) * BM + i % (BM / 4) * 4;
+            const int64_t o = static_cast<int64_t>(at.b0 + i / (BM / 4)) * p.ldy + j;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float sum = u[0][k];
+#pragma unroll
+                for (int s = 1; s < kMaxSplit; ++s)
+                    if (s < p.split)
+                        sum += u[s][k];
                 sum = sum * ta * tw;
+                if (j + k >= p.d_out)
+                    break;
                 if (p.yt == LNQ_BF16)
-                    static_cast<__nv_bfloat16 *>(p.y)[o] = from_f32<__nv_bfloat16>(sum);
+                    static_cast<__nv_bfloat16 *>(p.y)[o + k] = from_f32<__nv_bfloat16>(sum);
                 else if (p.yt == LNQ_F16)
-                    static_cast<__half *>(p.y)[o] = from_f32<__half>(sum);
+                    static_cast<__half *>(p.y)[o + k] = from_f32<__half>(sum);
                 else
-                    static_cast<float *>(p.y)[o] = sum;
+                    static_cast<float *>(p.y)[o + k] = sum;
             }
         }
     }
