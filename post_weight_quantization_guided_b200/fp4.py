@@ -24,6 +24,7 @@ EXPORTED = ("lnq_fp4_code_bytes", "lnq_fp4_scale_bytes", "lnq_fp4_tensor_scale",
 
 _VP, _I64, _INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 _lib = None
+_entry = {}  # name -> entry point, once loaded
 
 
 def lib():
@@ -47,6 +48,7 @@ def lib():
         L.lnq_fp4_check.argtypes = [_VP]
         for name in EXPORTED[2:]:
             getattr(L, name).restype = _INT
+            _entry[name] = getattr(L, name)
         _lib = L
     return _lib
 
@@ -63,7 +65,7 @@ def lnq_fp4_scale_bytes(d: int, fmt: int) -> int:
 
 def _need(t, dtype, shape, name, device):
     """A contiguous CUDA tensor of this type and shape, on `device`."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not device.type == "cuda" \
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda \
             or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -106,11 +108,15 @@ def _pitches(d, fmt) -> Tuple[int, int]:
     return pad * 64, pad * (4 if fmt == LNQ_FP4_MX else 8)
 
 
-def _codes(codes, scales, d, fmt, name, device, lead):
+def _codes(codes, scales, d, fmt, names, device, lead):
     """Checks the stored form of matrices [*lead][d]."""
     of_codes, of_scales = _pitches(d, fmt)
-    _need(codes, torch.uint8, (*lead, of_codes), f"{name} codes", device)
-    _need(scales, torch.uint8, (*lead, of_scales), f"{name} scales", device)
+    _need(codes, torch.uint8, (*lead, of_codes), names[0], device)
+    _need(scales, torch.uint8, (*lead, of_scales), names[1], device)
+
+
+_INPUT, _WEIGHT = ("codes", "scales"), ("weight codes", "weight scales")
+_ACTIVATION = ("activation codes", "activation scales")
 
 
 def _scale(t, count, fmt, name, device):
@@ -148,11 +154,12 @@ def _call(name, device, stream, *args):
         raise ValueError(f"{name}: the stream is of {stream.device}, the tensors are on {device}")
     else:
         handle = stream.cuda_stream
+    entry = _entry.get(name) or getattr(lib(), name)
     if torch._C._cuda_getDevice() == index:
-        status = getattr(lib(), name)(*args, handle)
+        status = entry(*args, handle)
     else:
         with torch.cuda.device(index):
-            status = getattr(lib(), name)(*args, handle)
+            status = entry(*args, handle)
     if status:
         raise LnqError(status, name)
 
@@ -198,7 +205,7 @@ def lnq_fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int, fmt: i
     """The values [rows][d] that (codes, scales) stand for; `dtype` is y's where y is given."""
     fmt, d, dev = _format(fmt), int(d), codes.device
     rows = codes.shape[0]
-    _codes(codes, scales, d, fmt, "input", dev, (rows,))
+    _codes(codes, scales, d, fmt, _INPUT, dev, (rows,))
     ts = _scale(tensor_scale, 1, fmt, "tensor_scale", dev)
     y, yt, ldy = _output(y, codes, (rows, d), dtype)
     _call("lnq_fp4_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, d, fmt, ts,
@@ -215,12 +222,12 @@ def _offsets(offsets, experts, device):
 def _gemv(name, x, offsets, codes, scales, fmt, tensor_scale, y, dtype, stream):
     xt, ldx = _dense(x, "x")
     fmt, (n, d_in), dev = _format(fmt), x.shape, x.device
-    lead = tuple(codes.shape[:-1])
+    lead = codes.shape[:-1]
     grouped = offsets is not None
     if len(lead) != 1 + grouped:
         raise ValueError(f"codes: expected {'[experts][d_out][bytes]' if grouped else '[d_out][bytes]'}"
                          f", got {tuple(codes.shape)}")
-    _codes(codes, scales, d_in, fmt, "weight", dev, lead)
+    _codes(codes, scales, d_in, fmt, _WEIGHT, dev, lead)
     ts = _scale(tensor_scale, lead[0] if grouped else 1, fmt, "tensor_scale", dev)
     if grouped:
         _offsets(offsets, lead[0], dev)
@@ -256,13 +263,13 @@ def _gemm(name, a_codes, a_scales, offsets, codes, scales, d_in, fmt, a_scale, b
     if d_in < 1:
         raise ValueError(f"d_in: expected at least 1, got {d_in}")
     n = a_codes.shape[0]
-    lead = tuple(codes.shape[:-1])
+    lead = codes.shape[:-1]
     grouped = offsets is not None
     if len(lead) != 1 + grouped:
         raise ValueError(f"codes: expected {'[experts][d_out][bytes]' if grouped else '[d_out][bytes]'}"
                          f", got {tuple(codes.shape)}")
-    _codes(a_codes, a_scales, d_in, fmt, "activation", dev, (n,))
-    _codes(codes, scales, d_in, fmt, "weight", dev, lead)
+    _codes(a_codes, a_scales, d_in, fmt, _ACTIVATION, dev, (n,))
+    _codes(codes, scales, d_in, fmt, _WEIGHT, dev, lead)
     ta = _scale(a_scale, 1, fmt, "a_scale", dev)
     tb = _scale(b_scale, lead[0] if grouped else 1, fmt, "b_scale", dev)
     if grouped:

@@ -615,6 +615,88 @@ def test_results_do_not_change_from_run_to_run(lnq):
         assert torch.equal(z, lnq.lnq_fp4_gemv(x[:9], w, s, MX, dtype=torch.float32))
 
 
+@pytest.mark.parametrize("n,d_in,d_out", [(20, 1024, 300), (60, 2048, 500), (128, 512, 9000),
+                                          (300, 1000, 700), (40, 2944, 300)])
+def test_a_wait_that_gives_up_is_reported(lnq, n, d_in, d_out):
+    """With no time for any wait, the product returns, the check says so once, and the next call is
+    whole again."""
+    rng = _rng(41, n)
+    ac, as_ = ref.random_stored(rng, (n,), d_in, NV, True)
+    ac &= 0x33
+    as_[:] = 56
+    wc, ws = ref.random_stored(rng, (d_out,), d_in, NV, True)
+    args = [dev(v) for v in (ac, as_, wc, ws)]
+    want = dev(ref.values(ac, as_, d_in, NV)) @ dev(ref.values(wc, ws, d_in, NV)).T
+    assert lnq.lnq_fp4_check() == 0
+    lnq.lnq_set_wait_limit(0)
+    try:
+        lnq.lnq_fp4_gemm(*args, d_in, NV, dtype=torch.float32)
+        assert lnq.lnq_fp4_check() == 5  # LNQ_ERR_TIMEOUT
+    finally:
+        lnq.lnq_set_wait_limit(-1)
+    assert lnq.lnq_fp4_check() == 0
+    assert torch.equal(lnq.lnq_fp4_gemm(*args, d_in, NV, dtype=torch.float32).double(), want)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_scales_at_their_least_alignment(lnq, fmt):
+    """Matrices that begin one row into their storage: scales 4 (MX) or 8 (NV) bytes off 16."""
+    rng = _rng(42)
+    for d_in in (100, 300, 512):
+        ac, as_ = ref.random_stored(rng, (41,), d_in, fmt, True)
+        ac &= 0x33
+        as_[:] = 127 if fmt == MX else 56
+        wc, ws = ref.random_stored(rng, (131,), d_in, fmt, True)
+        a, sa, w, sw = [dev(v)[1:] for v in (ac, as_, wc, ws)]
+        x, v = ref.values(ac[1:], as_[1:], d_in, fmt), ref.values(wc[1:], ws[1:], d_in, fmt)
+        check_product(lnq.lnq_fp4_gemm(a, sa, w, sw, d_in, fmt, dtype=torch.float32), x, v, exact=True)
+        check_product(lnq.lnq_fp4_gemv(dev(x, torch.float32)[:5], w, sw, fmt), x[:5], v, exact=True)
+        assert np.array_equal(f64(lnq.lnq_fp4_dequantize(w, sw, d_in, fmt)), v)
+
+
+def test_a_stream_given_by_the_caller(lnq):
+    x = torch.randn(64, 256, device="cuda")
+    w, s = lnq.lnq_fp4_quantize(x, MX)
+    want = lnq.lnq_fp4_gemv(x[:4], w, s, MX)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    y = torch.zeros(4, 64, device="cuda")
+    torch.cuda.synchronize()
+    lnq.lnq_fp4_gemv(x[:4], w, s, MX, y=y, stream=st)
+    st.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_matrices_beyond_32_bits(lnq):
+    """Codes, activations and results whose offsets pass 2^32 bytes: the last rows are those of
+    small calls."""
+    d, rows = 4096, 1_150_000                        # 9.4 GB of bf16, 2.4 GB of codes
+    x = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
+    x[:] = torch.randn(d, device="cuda")
+    x[-3:] = torch.randn(3, d, device="cuda")
+    codes, scales = lnq.lnq_fp4_quantize(x, MX)
+    c3, s3 = lnq.lnq_fp4_quantize(x[-3:].clone(), MX)
+    assert torch.equal(codes[-3:], c3) and torch.equal(scales[-3:], s3)
+    x.zero_()
+    lnq.lnq_fp4_dequantize(codes, scales, d, MX, y=x)
+    assert torch.equal(x[-3:], lnq.lnq_fp4_dequantize(c3, s3, d, MX, dtype=torch.bfloat16))
+    top = lnq.lnq_fp4_tensor_scale(x)
+    x[-1, -1] = 1000.0
+    assert lnq.lnq_fp4_tensor_scale(x).item() == float(np.float32(1000.0 / 2688)) != top.item()
+    del x
+    # as weights: 1.15 million outputs
+    a = torch.randn(2, d, device="cuda").bfloat16()
+    ac, as_ = lnq.lnq_fp4_quantize(a, MX)
+    assert torch.equal(lnq.lnq_fp4_gemm(ac, as_, codes, scales, d, MX)[:, -3:],
+                       lnq.lnq_fp4_gemm(ac, as_, c3, s3, d, MX))
+    check_product(lnq.lnq_fp4_gemv(a, codes, scales, MX)[:, -3:], f64(a),
+                  f64(lnq.lnq_fp4_dequantize(c3, s3, d, MX)))
+    # as activations: 1.15 million rows, 3000 outputs (6.9 GB)
+    w, s = lnq.lnq_fp4_quantize(torch.randn(3000, d, device="cuda"), MX)
+    y = lnq.lnq_fp4_gemm(codes, scales, w, s, d, MX)
+    assert torch.equal(y[-3:], lnq.lnq_fp4_gemm(codes[-259:], scales[-259:], w, s, d, MX)[-3:])
+
+
 def test_no_rows(lnq):
     for fmt in (MX, NV):
         x = torch.zeros(0, 100, device="cuda")
