@@ -36,7 +36,7 @@ constexpr int kRows = 16;        // outputs of a tile
 constexpr int kChunk = 128;      // elements of K a warp takes at a time
 constexpr int kAhead = 4;        // chunks whose codes a warp has in flight
 constexpr int kMaxShares = 8;    // CTAs of a cluster
-constexpr int kXBytes = 100000;  // shared memory for x: two CTAs fit an SM
+constexpr int kXBytes = 92 << 10;  // shared memory for x: two CTAs fit an SM
 
 template <typename T> struct Pieces;
 template <> struct Pieces<__nv_bfloat16> { static constexpr int n = 1; };
@@ -169,7 +169,7 @@ __device__ __forceinline__ uint32_t scale_rest(uint32_t v)
     return (max(v, kTopScale) - kTopScale + 127u) * 0x00800080u;
 }
 
-// NT column tiles (of 8 / pieces rows of x) per pass over the weights. Grid: x = clusters per
+// NT tiles of 8 columns (pieces of rows of x) per pass over the weights. Grid: x = clusters per
 // expert times the cluster's CTAs, y = experts. `parts` warps share a tile's K within a CTA,
 // `shares` CTAs within a cluster; `panel` chunks of x fit at a time.
 template <typename TX, int FMT, int NT>
@@ -179,8 +179,7 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                     int yt, int64_t ldy, int parts, int shares, int panel)
 {
     using namespace gv;
-    constexpr int P = Pieces<TX>::n, kTok = 8 / P;   // rows of x per column tile
-    constexpr int kPass = NT * kTok;                 // and per pass
+    constexpr int P = Pieces<TX>::n, kPass = NT * 8 / P;  // rows of x per pass: P columns each
     constexpr int kBlocks = 32 / fp4_block(FMT);     // blocks of a lane's 32 elements
     // With one column tile the multipliers come from a table (83 us where computing them takes
     // 87, 16 rows over 8 experts 4096 -> 14336); with more, shared memory is busy with x (69 and 54).
@@ -211,29 +210,25 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
     const int slots = kWarps / parts, slot = warp / parts, part = warp % parts;
     const int rounds = ((tiles - cluster + clusters - 1) / clusters + slots - 1) / slots;
     const bool once = c_end - c_begin <= panel;  // x fits at once
-    // columns in use: one tile of few rows keeps only those
-    const int tokens = NT > 1 ? kTok : min(kTok, rows.y - rows.x), columns = NT > 1 ? 8 : tokens * P;
+    // columns kept of each tile: one tile of few rows keeps only theirs
+    const int columns = NT > 1 ? 8 : min(kPass, rows.y - rows.x) * P;
 
     for (int b0 = rows.x; b0 < rows.y; b0 += kPass) {
+        const int tokens = min(kPass, rows.y - b0);
         auto stage = [&](int c0, int c1) {  // x of chunks c0 .. c1 - 1
-            for (int i = threadIdx.x; i < (c1 - c0) * NT * 16 * tokens; i += kThreads) {
-                const int q = i / tokens, token = i - q * tokens;  // q: [chunk][nt][word][t]
-                const int c = q / (NT * 16), nt = q / 16 % NT, b = b0 + nt * kTok + token;
-                const int k = (c0 + c) * kChunk + (q & 3) * 32 + (q >> 2 & 3) * 8;
-                if (b >= rows.y)  // nobody reads its sums
-                    continue;
+#pragma unroll 2
+            for (int i = threadIdx.x; i < (c1 - c0) * 16 * tokens; i += kThreads) {
+                const int q = i / tokens, token = i - q * tokens;  // q: [chunk][word][t]
+                const int c = q / 16, k = (c0 + c) * kChunk + (q & 3) * 32 + (q >> 2 & 3) * 8;
                 uint4 col[P];
-                load_columns<TX>(x + (k < d_in ? b * ldx + k : 0), d_in - k, wide, col);
+                load_columns<TX>(x + (k < d_in ? (b0 + token) * ldx + k : 0), d_in - k, wide, col);
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    xs[q * columns + token * P + p] = col[p];
+                for (int p = 0; p < P; ++p) {
+                    const int at = token * P + p;  // column of the pass
+                    xs[((c * NT + at / 8) * 16 + q % 16) * columns + at % 8] = col[p];
+                }
             }
         };
-        __syncthreads();  // the last pass has read x; the multipliers are written
-        if (once) {
-            stage(c_begin, c_end);
-            __syncthreads();
-        }
         const uint8_t *codes0, *codes1, *scales0, *scales1;
         Chunk ring[kAhead];
         auto fetch = [&](Chunk &q, int ahead, int left) {
@@ -267,7 +262,12 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                 fetch(ring[u], u, w_end - w_begin - u);
         };
         if (once)
-            begin(tile_of(0), c_begin, c_end);
+            begin(tile_of(0), c_begin, c_end);  // its loads run while x is written
+        __syncthreads();  // the last pass has read x; the multipliers are written
+        if (once) {
+            stage(c_begin, c_end);
+            __syncthreads();
+        }
         for (int round = 0; round < rounds; ++round) {
             const bool mine = tile_of(round) < tiles;
             float acc[NT][4];
@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                 if (!mine)
                     continue;
                 const int w_begin = p0 + part * (p1 - p0) / parts, w_end = p0 + (part + 1) * (p1 - p0) / parts;
+                // a column that no row has repeats another: nobody reads its sums
                 const uint4 *xc = xs + (w_begin - p0) * (NT * 16) * columns + t * columns + min(g, columns - 1);
-                const bool has = g < columns;
                 for (int c0 = w_begin; c0 < w_end; c0 += kAhead) {
 #pragma unroll
                     for (int u = 0; u < kAhead; ++u) {
@@ -325,9 +325,7 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                                if (NT > 1 || has)
-                                    v = xc[(nt * 16 + j * 4) * columns];
+                                const uint4 v = xc[(nt * 16 + j * 4) * columns];
                                 mma_bf16(acc[nt], lo, v.x, v.y);
                                 mma_bf16(acc[nt], hi, v.z, v.w);
                             }
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
 #pragma unroll
                 for (int p = P - 1; p >= 0; --p)  // the small pieces first
                     for (int q = 0; q < parts; ++q)
-                        sum = sum_at(sum, &sums[k * parts + q][r][b / kTok * 8 + b % kTok * P + p]);
+                        sum = sum_at(sum, &sums[k * parts + q][r][b * P + p]);
                 sum *= scale;
                 const int64_t o = static_cast<int64_t>(b0 + b) * ldy + j;
                 if (yt == LNQ_BF16)
@@ -479,6 +477,8 @@ static cudaError_t gemv_fmt(const void *x, int n, int64_t ldx, const int32_t *of
         return gemv_tiles<TX, FMT, 1>(x, n, ldx, offsets, experts, w, d_in, y, yt, ldy, num_sms, s);
     if (tiles <= 2)
         return gemv_tiles<TX, FMT, 2>(x, n, ldx, offsets, experts, w, d_in, y, yt, ldy, num_sms, s);
+    if (tiles <= 3)
+        return gemv_tiles<TX, FMT, 3>(x, n, ldx, offsets, experts, w, d_in, y, yt, ldy, num_sms, s);
     return gemv_tiles<TX, FMT, 4>(x, n, ldx, offsets, experts, w, d_in, y, yt, ldy, num_sms, s);
 }
 
