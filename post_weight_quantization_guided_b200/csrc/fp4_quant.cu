@@ -5,8 +5,8 @@
 //
 // Bound: HBM (read x, write half a byte an element). One pass: a lane takes 16 consecutive
 // elements, an NV block or half an MX one (whose two lanes agree on its largest element by a
-// shuffle), a warp 512 elements of a row. NV is bound by its two roundings instead (61 us for
-// 16384 x 4096 bf16, where MX takes 35 and its bytes 26).
+// shuffle), a warp 512 elements of a row. 16384 x 4096 bf16 elements take 31 us (MX; their bytes 26) and
+// 41 us (NV: two roundings and the ties).
 //
 // Exact decisions. MX quotients are exact (a power of two). An NV quotient is estimated in 32 bits
 // and rounded twice, a little below and a little above the estimate; where both agree that is the
@@ -211,15 +211,21 @@ __device__ __forceinline__ uint32_t nv_scale_byte(float amax, const MatrixScale 
     return m.fast && byte == (both >> 8) ? byte : nv_scale_exact(amax, m.t);
 }
 
-// The codes of an NV block's 16 elements with scale s, any t: quotients in 64 bits. A quotient on a
-// border of two codes is exact; any other is at least 2^-31 away from it, further than its rounding.
-__device__ __noinline__ uint2 nv_codes_slow(const float *v, float s, float t)
+// The codes of an NV block (its first `left` elements at x) with scale s, any t: quotients in 64
+// bits. A quotient on a border of two codes is exact; any other is at least 2^-31 away from it,
+// further than its rounding. (The elements are read again: handing over registers would have
+// every block written to local memory, which took half of the kernel's time.)
+template <typename T>
+__device__ __noinline__ uint2 nv_codes_slow(const T *__restrict__ x, int left, float s, float t)
 {
     const double step = static_cast<double>(s) * static_cast<double>(t);
-    float q[kLane];
-    for (int k = 0; k < kLane; ++k)
-        q[k] = to_odd(fmax(-8.0, fmin(8.0, static_cast<double>(v[k]) / step)));
-    return make_uint2(e2m1x8(q), e2m1x8(q + 8));
+    uint32_t word[2] = {0u, 0u};
+    for (int k = 0; k < min(left, kLane); ++k) {
+        float q[8] = {};
+        q[0] = to_odd(fmax(-8.0, fmin(8.0, static_cast<double>(to_f32<T>(x[k])) / step)));
+        word[k >> 3] |= e2m1x8(q) << (4 * (k & 7));
+    }
+    return make_uint2(word[0], word[1]);
 }
 
 // v[k] * r for pairs, packed.
@@ -236,35 +242,42 @@ __device__ __forceinline__ void scale16(const float (&v)[kLane], float r, float 
     }
 }
 
-__device__ __forceinline__ uint2 nv_codes(const float (&v)[kLane], float s, const MatrixScale &m)
+// The codes of an NV block with scale s; v are its elements, x where they (the first `left`) are.
+template <typename T>
+__device__ __forceinline__ uint2 nv_codes(const float (&v)[kLane], const T *__restrict__ x, int left, float s,
+                                          const MatrixScale &m)
 {
     if (!m.fast)
-        return nv_codes_slow(v, s, m.t);
+        return nv_codes_slow<T>(x, left, s, m.t);
     // relative error of v * r below 2^-21: three roundings and the approximate reciprocal
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     r *= m.rt;
     float q[kLane];
     scale16(v, r * (1.f - 0x1p-20f), q);
-    const uint2 below = make_uint2(e2m1x8(q), e2m1x8(q + 8));
+    uint2 codes = make_uint2(e2m1x8(q), e2m1x8(q + 8));
     scale16(v, r * (1.f + 0x1p-20f), q);
-    const uint2 above = make_uint2(e2m1x8(q), e2m1x8(q + 8));
-    if (below.x != above.x || below.y != above.y) {
-        // Some quotient is near a border. A border has three significant bits, so the one near a
-        // quotient is the quotient rounded to three; the sign of |v| - (b s) t is exact. A quotient
-        // off the border is moved away from it, to that side, by more than its error and less than
-        // the way to any other; one that is on it becomes the border, a tie.
-#pragma unroll
-        for (int k = 0; k < kLane; ++k) {
-            const float e = v[k] * r;
-            const float b = __uint_as_float((__float_as_uint(e) + 0x00100000u) & 0xFFE00000u);
-            const float d = fmaf(-b * s, m.t, v[k]);
-            const uint32_t sign = (__float_as_uint(d) ^ __float_as_uint(v[k])) & 0x80000000u;
-            q[k] = d == 0.f ? b : e * (1.f + __uint_as_float(sign | 0x36000000u));  // 2^-19
+    uint32_t d0 = codes.x ^ e2m1x8(q), d1 = codes.y ^ e2m1x8(q + 8);
+    // Where they differ the border between codes c and c + 1 decides, one element at a time (few
+    // lanes have more than one).
+    while ((d0 | d1) != 0u) {
+        const bool second = d0 == 0u;
+        const int shift = (__ffs(static_cast<int>(second ? d1 : d0)) - 1) & ~3;
+        const uint32_t c = ((second ? codes.y : codes.x) >> shift) & 7u;
+        const float e = fabsf(to_f32<T>(x[(second ? 8 : 0) + shift / 4]));
+        const float b = 0.5f * (fp4_code_value(c) + fp4_code_value(c + 1u));
+        const float d = fmaf(-b * s, m.t, e);
+        const uint32_t up = d > 0.f || (d == 0.f && (c & 1u)) ? 1u << shift : 0u;
+        const uint32_t done = ~(15u << shift);
+        if (second) {
+            codes.y += up;
+            d1 &= done;
+        } else {
+            codes.x += up;
+            d0 &= done;
         }
-        return make_uint2(e2m1x8(q), e2m1x8(q + 8));
     }
-    return below;
+    return codes;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -305,7 +318,8 @@ __global__ void __launch_bounds__(kQuantThreads)
             if (amax < 0x7F800000u && m.valid) {
                 byte = nv_scale_byte(__uint_as_float(amax), m);
                 if (byte != 0u)
-                    word = nv_codes(v, __uint_as_float(byte << 20) * 0x1p120f, m);
+                    word = nv_codes<T>(v, x + walk.row * ldx + i0, d - i0,
+                                       __uint_as_float(byte << 20) * 0x1p120f, m);
             }
         }
         if (i0 < padded) {
