@@ -86,8 +86,8 @@ LNQ_API lnq_status lnq_fp4_dequantize(const uint8_t *codes, const uint8_t *scale
                                       lnq_dtype yt, int64_t ldy, lnq_stream_t stream);
 
 /* y[b][j] = sum_i x[b][i] w[j][i] for b < nb: unquantised activations times a quantised matrix,
- * for the few rows of a decoding step (any nb >= 0 is taken; the weights are read once per 32
- * rows, and lnq_fp4_gemm is the operator for prompts).
+ * for the few rows of a decoding step (any nb >= 0 is taken; the weights are read once for every
+ * 32 rows of bf16, 16 of f16 or 10 of f32 x, and lnq_fp4_gemm is the operator for prompts).
  *   x [nb][ldx] of type xt; codes, scales [d_out] rows of d_in; y [nb][ldy] of type yt, out.
  * Arithmetic: every product is exact (bits of a 32-bit x below 2^-133 may be dropped), the sums
  * are 32-bit, t multiplies the finished sum, and y is rounded once to its type. */

@@ -62,12 +62,13 @@ template <> __device__ __forceinline__ __half from_f32<__half>(float v)
 }
 
 // offsets[] as the grouped operators read it: each value limited to 0 .. n and to no less than
-// the largest before it. Returns group e's first row and the row behind its last.
+// the largest before it. Returns group e's first row and the row behind its last. For whole warps.
 __device__ __forceinline__ int2 fp4_group_rows(const int32_t *__restrict__ offsets, int e, int n)
 {
     int lo = 0;
-    for (int i = 0; i <= e; ++i)
+    for (int i = threadIdx.x & 31; i <= e; i += 32)
         lo = max(lo, min(offsets[i], n));
+    lo = __reduce_max_sync(0xffffffffu, lo);
     return make_int2(lo, max(lo, min(offsets[e + 1], n)));
 }
 
