@@ -22,7 +22,7 @@
 // Warps: 0-7 epilogue (two per TMEM lane quarter, alternate 32-column chunks), 8 loads, 9-10 scales,
 // 11 MMA. Persistent over tiles, outputs fastest, so that neighbouring pairs
 // share the rows' tile.
-// With few tiles, `split` pairs of one cluster take a share of K each and add their sums through
+// With few tiles, two pairs of one cluster take half of K each and add their sums through
 // distributed shared memory in a fixed order.
 #include <cstring>
 
@@ -43,7 +43,7 @@ constexpr int kTmaWarp = 8, kLoadWarp = 9, kScaleWarp = 10, kMmaWarp = 11;
 constexpr int kThreads = 12 * 32;       // 168 registers a thread
 constexpr int kScaleRing = 4;           // steps (two stages each) of scales in flight
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxSplit = 4;            // pairs of a cluster
+constexpr int kMaxSplit = 2;            // pairs of a cluster
 constexpr int kAtom = 512;              // bytes of scales of 128 rows x 4 blocks
 
 template <int BN, int FMT>
@@ -736,18 +736,44 @@ cudaError_t fp4_gemm_launch(const Fp4Matrix &a, const int32_t *offsets, int64_t 
     p.scale_pitch = static_cast<int>(fp4_scale_pitch(d_in, fmt));
     p.mt = static_cast<int>((w.rows + f4::PM - 1) / f4::PM);
     p.limit = wait_limit;
-    // rows per tile: the narrowest that holds a group of average size
-    const int64_t mean = (a.rows + experts - 1) / experts;
-    const int bn = mean <= 32 ? 32 : (mean <= 64 ? 64 : (mean <= 128 ? 128 : 256));
-    // an upper bound where the groups are not known here
-    const int64_t row_tiles = offsets == nullptr ? (a.rows + bn - 1) / bn
-                                                 : min(a.rows, a.rows / bn + experts);
-    const int64_t tiles = row_tiles * p.mt;
+    // an upper bound of the row tiles where the groups are not known here
+    auto tiles_of = [&](int rows) {
+        return p.mt * (offsets == nullptr ? (a.rows + rows - 1) / rows
+                                          : min(a.rows, a.rows / rows + experts));
+    };
     const int64_t pairs = num_sms / 2;
+    int bn = 32;
     p.split = 1;
-    if (offsets == nullptr && bn <= 128)
-        while (p.split < f4::kMaxSplit && tiles * p.split * 2 <= pairs && p.nk >= p.split * 4)
-            p.split *= 2;
+    if (offsets != nullptr) {
+        // Twice a group of average size, 64 at least: a tile's time depends little on its width,
+        // and a group larger than the tile reads its weights again (2000 rows over 32 experts,
+        // 2048 -> 2048, largest group 493: 31 us with 64 rows a tile, 24 with 128, 25 with 256).
+        const int64_t mean = (a.rows + experts - 1) / experts;
+        bn = 64;
+        while (bn < 256 && bn < 2 * mean)
+            bn *= 2;
+    } else {
+        // Rows per tile and pairs that share a tile's K: the least time, in hundredths of a
+        // microsecond, from the times measured for a tile's fixed parts (first loads, last sums;
+        // joining the shares) and for a stage, which depends little on the width. (Four pairs to
+        // a tile, clusters of 8, were slower than two at every size.)
+        constexpr int kFixed[4] = {540, 590, 690, 820}, kStage[4] = {38, 39, 40, 43};
+        int64_t best = INT64_MAX;
+        for (int w = 0; w < 4; ++w) {
+            const int rows = 32 << w;
+            const int64_t tiles = tiles_of(rows);
+            for (int split = 1; split <= (rows <= 128 ? f4::kMaxSplit : 1); split *= 2) {
+                if (split > 1 && (tiles * split > pairs || p.nk < split * 2))
+                    break;
+                const int64_t cost = (tiles * split + pairs - 1) / pairs *
+                                         ((p.nk + split - 1) / split * kStage[w]) + kFixed[w] +
+                                     (split > 1 ? 60 : 0);
+                if (cost < best)
+                    best = cost, bn = rows, p.split = split;
+            }
+        }
+    }
+    const int64_t tiles = tiles_of(bn);
     const bool nv = fmt == LNQ_FP4_NV;
     switch (bn) {
     case 32:
