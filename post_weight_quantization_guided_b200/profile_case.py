@@ -12,7 +12,9 @@ With `--fisher-only` it stops after building the blocks twice (`--tokens` shorte
 vector (the codes cycled through enough copies that they come from HBM). With `--diag N` it runs
 N calls of LNQ with diagonal Fisher blocks (the diagonals of the blocks just built, `--iters`
 iterations each, from the initial codebooks). With `--ganq N` it runs N calls of the GANQ-style
-comparison solver (`--iters` iterations each, from the initial codebooks).
+comparison solver (`--iters` iterations each, from the initial codebooks). With `--fp4 N` it
+quantises W once and then, N times, quantises X, multiplies the two on the block-scaled tensor
+cores, and multiplies the first token alone with the 4-bit weights.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ import argparse
 import torch
 
 from . import binding as api
+from . import fp4
 from . import workloads as wl
 
 WORKLOADS = {"tiny": wl.TINY, "q_proj": wl.Q_PROJ, "down_proj": wl.DOWN_PROJ, "up_proj": wl.UP_PROJ,
@@ -38,6 +41,8 @@ def main(argv=None) -> None:
                     help="calls of LNQ with diagonal Fisher blocks after the run")
     ap.add_argument("--ganq", type=int, default=0,
                     help="calls of the GANQ-style comparison solver after the run")
+    ap.add_argument("--fp4", type=int, default=0,
+                    help="rounds of the microscaled 4-bit operators after the run")
     ap.add_argument("--fisher-only", action="store_true",
                     help="build the Fisher blocks (twice) and stop")
     ap.add_argument("--tokens", type=int, default=0, help="calibration tokens (default: the workload's)")
@@ -93,6 +98,17 @@ def main(argv=None) -> None:
             api.lnq_ganq_rows(F, W, layer.m, args.iters, C, Q, J, st)
         torch.cuda.synchronize()
         print(f"ganq calls={args.ganq} iters={args.iters} sum(J)={float(J.sum()):.6e}")
+    if args.fp4:
+        fmt = fp4.LNQ_FP4_NV
+        tw, tx = fp4.lnq_fp4_tensor_scale(W), fp4.lnq_fp4_tensor_scale(X)
+        w, ws = fp4.lnq_fp4_quantize(W, fmt, tensor_scale=tw)
+        for _ in range(args.fp4):
+            x, xs = fp4.lnq_fp4_quantize(X, fmt, tensor_scale=tx)
+            y = fp4.lnq_fp4_gemm(x, xs, w, ws, layer.d_in, fmt, a_scale=tx, b_scale=tw)
+            z = fp4.lnq_fp4_gemv(X[:1], w, ws, fmt, tensor_scale=tw)
+        torch.cuda.synchronize()
+        print(f"fp4 rounds={args.fp4} check={fp4.lnq_fp4_check()} "
+              f"sum(y)={float(y.float().sum()):.6e} sum(z)={float(z.float().sum()):.6e}")
 
 
 if __name__ == "__main__":
