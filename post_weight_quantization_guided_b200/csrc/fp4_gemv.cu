@@ -6,7 +6,7 @@
 // Bound: HBM, the codes and scales read once (half a byte and 1/16 (NV) or 1/32 (MX) of a byte an
 // element); in practice the decoding, about 3.6 instructions an element (integer pipe 56% busy). One
 // B200: 16 rows over 8 experts 4096 -> 14336 80 us (3.3 TB/s of codes and scales), 1 x 4096 -> 14336
-// 14 us, 1 x 4096 -> 4096 7.4 us, 7 x 11008 -> 4101 in 32 bits 35 us.
+// 14 us, 1 x 4096 -> 4096 7.4 us, 7 x 11008 -> 4101 in 32 bits 22 us.
 //
 // The products run on mma.sync m16n8k16 in bf16 with 32-bit sums: with at most a few rows the
 // work is decoding weights, and the instruction takes them straight from registers, where
@@ -37,6 +37,7 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRows = 16;        // outputs of a tile
 constexpr int kChunk = 128;      // elements of K a warp takes at a time
 constexpr int kAhead = 4;        // chunks whose codes a warp has in flight
+constexpr int kSumPitch = kRows + 4;  // a warp's two columns by 8 outputs fall into different banks
 constexpr int kMaxShares = 8;    // CTAs of a cluster
 constexpr int kXBytes = 92 << 10;  // shared memory for x: two CTAs fit an SM
 
@@ -183,19 +184,18 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
     using namespace gv;
     constexpr int P = Pieces<TX>::n, kPass = NT * 8 / P;  // rows of x per pass: P columns each
     constexpr int kBlocks = 32 / fp4_block(FMT);     // blocks of a lane's 32 elements
-    // With one column tile the multipliers come from a table (83 us where computing them takes
-    // 87, 16 rows over 8 experts 4096 -> 14336); with more, shared memory is busy with x (69 and 54).
-    constexpr bool kTable = NT == 1;
-    extern __shared__ uint4 xs[];                    // [panel][NT][4 words][4 lanes t][columns]
-    __shared__ float sums[kWarps][kRows][NT * 8 + 1];
-    __shared__ uint32_t multiplier[kTable ? 256 : 1];  // of each scale byte
+    // x: a word's 8 columns by 4 lanes t in the order of the lanes that read them
+    extern __shared__ uint4 xs[];  // [panel][NT][4 words][columns][4 lanes t]
+    __shared__ float sums[kWarps][NT * 8][kSumPitch];
+    // the multiplier of each scale byte (83 us where computing them takes 87, 16 rows over 8 experts
+    // 4096 -> 14336; 37 and 39, 10 rows in 32 bits)
+    __shared__ uint32_t multiplier[256];
     const int e = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int2 rows = offsets == nullptr ? make_int2(0, n) : fp4_group_rows(offsets, e, n);
     if (rows.x >= rows.y)
         return;
-    if (kTable)
-        multiplier[threadIdx.x] = scale_pair<FMT>(threadIdx.x);
+    multiplier[threadIdx.x] = scale_pair<FMT>(threadIdx.x);
     const int share = shares > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int cluster = static_cast<int>(blockIdx.x) / shares, clusters = static_cast<int>(gridDim.x) / shares;
     const int d_out = static_cast<int>(w.rows), tiles = (d_out + kRows - 1) / kRows;
@@ -220,14 +220,14 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
         auto stage = [&](int c0, int c1) {  // x of chunks c0 .. c1 - 1
 #pragma unroll 2
             for (int i = threadIdx.x; i < (c1 - c0) * 16 * tokens; i += kThreads) {
-                const int q = i / tokens, token = i - q * tokens;  // q: [chunk][word][t]
-                const int c = q / 16, k = (c0 + c) * kChunk + (q & 3) * 32 + (q >> 2 & 3) * 8;
+                const int q = i & 15, r = i / 16, c = r / tokens, token = r - c * tokens;  // q: [word][t]
+                const int k = (c0 + c) * kChunk + (q & 3) * 32 + (q >> 2) * 8;
                 uint4 col[P];
                 load_columns<TX>(x + (k < d_in ? (b0 + token) * ldx + k : 0), d_in - k, wide, col);
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
                     const int at = token * P + p;  // column of the pass
-                    xs[((c * NT + at / 8) * 16 + q % 16) * columns + at % 8] = col[p];
+                    xs[(((c * NT + at / 8) * 4 + (q >> 2)) * columns + at % 8) * 4 + (q & 3)] = col[p];
                 }
             }
         };
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                     continue;
                 const int w_begin = p0 + part * (p1 - p0) / parts, w_end = p0 + (part + 1) * (p1 - p0) / parts;
                 // a column that no row has repeats another: nobody reads its sums
-                const uint4 *xc = xs + (w_begin - p0) * (NT * 16) * columns + t * columns + min(g, columns - 1);
+                const uint4 *xc = xs + (w_begin - p0) * (NT * 16) * columns + min(g, columns - 1) * 4 + t;
                 for (int c0 = w_begin; c0 < w_end; c0 += kAhead) {
 #pragma unroll
                     for (int u = 0; u < kAhead; ++u) {
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
 #pragma unroll
                         for (int k = 0; k < kBlocks; ++k) {
                             const uint32_t v0 = (q.s0 >> (8 * k)) & 255u, v1 = (q.s1 >> (8 * k)) & 255u;
-                            m0[k] = kTable ? multiplier[v0] : scale_pair<FMT>(v0);
-                            m1[k] = kTable ? multiplier[v1] : scale_pair<FMT>(v1);
+                            m0[k] = multiplier[v0];
+                            m1[k] = multiplier[v1];
                         }
                         const bool large = FMT == LNQ_FP4_MX &&
                                            __any_sync(0xffffffffu, max(q.s0, q.s1) > kTopScale);
@@ -346,23 +346,26 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
             if (mine) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    sums[warp][g][nt * 8 + 2 * t] = acc[nt][0];
-                    sums[warp][g][nt * 8 + 2 * t + 1] = acc[nt][1];
-                    sums[warp][g + 8][nt * 8 + 2 * t] = acc[nt][2];
-                    sums[warp][g + 8][nt * 8 + 2 * t + 1] = acc[nt][3];
+                    sums[warp][nt * 8 + 2 * t][g] = acc[nt][0];
+                    sums[warp][nt * 8 + 2 * t + 1][g] = acc[nt][1];
+                    sums[warp][nt * 8 + 2 * t][g + 8] = acc[nt][2];
+                    sums[warp][nt * 8 + 2 * t + 1][g + 8] = acc[nt][3];
                 }
             }
-            // output i of the round: tile slot, row of x, output of the tile
-            auto finish = [&](int i, auto &&sum_at) {
-                const int k = i / (kRows * kPass), b = i / kRows % kPass, r = i % kRows;
+            // Output i of the round: tile slot k, row b of x, output r of the tile.
+            // This CTA's sum: the small pieces first, of each the warps that share the tile.
+            auto own_sum = [&](int k, int b, int r) {
+                float sum = 0.f;
+#pragma unroll
+                for (int p = P - 1; p >= 0; --p)
+                    for (int q = 0; q < parts; ++q)
+                        sum += sums[k * parts + q][b * P + p][r];
+                return sum;
+            };
+            auto put = [&](int k, int b, int r, float sum) {
                 const int j = (cluster + (round * slots + k) * clusters) * kRows + r;
                 if (b0 + b >= rows.y || j >= d_out)
                     return;
-                float sum = 0.f;
-#pragma unroll
-                for (int p = P - 1; p >= 0; --p)  // the small pieces first
-                    for (int q = 0; q < parts; ++q)
-                        sum = sum_at(sum, &sums[k * parts + q][r][b * P + p]);
                 sum *= scale;
                 const int64_t o = static_cast<int64_t>(b0 + b) * ldy + j;
                 if (yt == LNQ_BF16)
@@ -372,30 +375,36 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                 else
                     static_cast<float *>(y)[o] = sum;
             };
+            __syncthreads();
+            for (int i = threadIdx.x; i < slots * kRows * kPass; i += kThreads) {
+                const int k = i / (kRows * kPass), b = i / kRows % kPass, r = i % kRows;
+                const float sum = own_sum(k, b, r);
+                if (shares == 1)
+                    put(k, b, r, sum);
+                else
+                    sums[k * parts][b * P][r] = sum;
+            }
             if (shares == 1) {
                 __syncthreads();
-                for (int i = threadIdx.x; i < slots * kRows * kPass; i += kThreads)
-                    finish(i, [](float s, const float *at) { return s + *at; });
-                __syncthreads();
-            } else {
-                cluster_sync();
-                for (int i = share * kThreads + threadIdx.x; i < slots * kRows * kPass; i += shares * kThreads)
-                    finish(i, [&](float s, const float *at) {
-                        float v[kMaxShares];
-#pragma unroll
-                        for (int q = 0; q < kMaxShares; ++q)
-                            if (q < shares)
-                                asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                             : "=f"(v[q])
-                                             : "r"(cluster_addr(at, static_cast<uint32_t>(q))));
-#pragma unroll
-                        for (int q = 0; q < kMaxShares; ++q)
-                            if (q < shares)
-                                s += v[q];
-                        return s;
-                    });
-                cluster_sync();  // the sums have been read
+                continue;
             }
+            cluster_sync();
+            for (int i = share * kThreads + threadIdx.x; i < slots * kRows * kPass; i += shares * kThreads) {
+                const int k = i / (kRows * kPass), b = i / kRows % kPass, r = i % kRows;
+                float v[kMaxShares], sum = 0.f;
+#pragma unroll
+                for (int q = 0; q < kMaxShares; ++q)
+                    if (q < shares)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(v[q])
+                                     : "r"(cluster_addr(&sums[k * parts][b * P][r], static_cast<uint32_t>(q))));
+#pragma unroll
+                for (int q = 0; q < kMaxShares; ++q)
+                    if (q < shares)
+                        sum += v[q];
+                put(k, b, r, sum);
+            }
+            cluster_sync();  // the sums have been read
         }
     }
 }
@@ -424,10 +433,12 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // How K is shared: by `shares` CTAs of a cluster (less of x for each to write) and `parts`
-    // warps of a CTA (fewer idle warps in the last round). The least time, in hundredths of a
-    // tile's chunk (0.65 us measured with two CTAs an SM): a chunk of x staged, a chunk of a tile, and
-    // a round's fixed costs, which are larger where a cluster's CTAs wait for one another.
-    constexpr int64_t kStage = NT * (Pieces<TX>::n == 1 ? 12 : 24), kWork = 80 + 20 * NT;
+    // warps of a CTA (fewer idle warps in the last round). The least time, in units of 6.5 ns, fitted
+    // to 15 sizes at all shares and parts, two CTAs an SM (it picks the fastest at each or one within
+    // 1% of it): a chunk of a column of x staged, a chunk of a tile, and a round's fixed costs,
+    // which are larger where a cluster's CTAs wait for one another.
+    constexpr int64_t kWork = 62 + 13 * NT, kRound = 390, kClusterRound = 530;
+    const int64_t stage = min((n + experts - 1) / experts, int64_t(NT * 8 / Pieces<TX>::n)) * Pieces<TX>::n * 4;
     static std::atomic<int> resident[4];  // clusters that run at once, by their size
     int shares = 1, parts = 1;
     int64_t clusters = 1, best = INT64_MAX;
@@ -438,7 +449,7 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
             if (c > 1) {
                 attr[0].val.clusterDim.x = static_cast<unsigned>(c);
                 cfg.gridDim = dim3(static_cast<unsigned>(room * c));
-                cfg.dynamicSmemBytes = kXBytes;
+                cfg.dynamicSmemBytes = kXBytes / kChunkBytes * kChunkBytes;
                 int active = 0;
                 if (cudaOccupancyMaxActiveClusters(&active, kernel, &cfg) == cudaSuccess && active > 0)
                     room = active;
@@ -452,8 +463,9 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
         for (int k = 1; k <= kWarps && (k == 1 || own >= k * 2); k *= 2) {
             const int64_t rounds = (per_cta * k + kWarps - 1) / kWarps;
             const int64_t stagings = own * kChunkBytes > kXBytes ? rounds : 1;
-            const int64_t cost = waves * (stagings * own * kStage +
-                                          rounds * ((own + k - 1) / k * kWork + (c > 1 ? 500 : 80)));
+            const int64_t cost = waves * (stagings * own * stage +
+                                          rounds * ((own + k - 1) / k * kWork +
+                                                    (c > 1 ? kClusterRound : kRound)));
             if (cost < best)
                 best = cost, shares = c, parts = k, clusters = m;
         }
