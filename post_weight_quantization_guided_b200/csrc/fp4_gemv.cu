@@ -4,8 +4,8 @@
 //   y[b][j] = t sum_k s[j][k] sum_{i in block k} x[b][i] code[j][i]
 //
 // Bound: HBM, the codes and scales read once (half a byte and 1/16 (NV) or 1/32 (MX) of a byte an
-// element); in practice the decoding, about 3.6 instructions an element (integer pipe 56% busy). One
-// B200: 16 rows over 8 experts 4096 -> 14336 80 us (3.3 TB/s of codes and scales), 1 x 4096 -> 14336
+// element); in practice the decoding, about 3.4 instructions an element (integer pipe 57% busy). One
+// B200: 16 rows over 8 experts 4096 -> 14336 73 us (3.6 TB/s of codes and scales), 1 x 4096 -> 14336
 // 14 us, 1 x 4096 -> 4096 7.4 us, 7 x 11008 -> 4101 in 32 bits 22 us.
 //
 // The products run on mma.sync m16n8k16 in bf16 with 32-bit sums: with at most a few rows the
@@ -172,20 +172,30 @@ __device__ __forceinline__ uint32_t scale_rest(uint32_t v)
     return (max(v, kTopScale) - kTopScale + 127u) * 0x00800080u;
 }
 
+// A round of a CTA: 2^log warps to each of its next tiles; the last tiles (1 or more) take all the
+// warps they can, as long as `chunks` of K give each two (16 rows over 8 experts 4096 -> 14336:
+// 73 us, 80 with its last tiles' other warps idle).
+__host__ __device__ __forceinline__ int gemv_round_log(int log, int tiles_left, int chunks)
+{
+    while (tiles_left > 0 && (tiles_left << (log + 1)) <= gv::kWarps && (chunks >> (log + 2)) > 0)
+        ++log;
+    return log;
+}
+
 // NT tiles of 8 columns (pieces of rows of x) per pass over the weights. Grid: x = clusters per
-// expert times the cluster's CTAs, y = experts. `parts` warps share a tile's K within a CTA,
-// `shares` CTAs within a cluster; `panel` chunks of x fit at a time.
+// expert times the cluster's CTAs, y = experts. 2^`part_log` warps (more in the last round) share a
+// tile's K within a CTA, `shares` CTAs within a cluster; `panel` chunks of x fit at a time.
 template <typename TX, int FMT, int NT>
 __global__ void __launch_bounds__(gv::kThreads, 2)
     fp4_gemv_kernel(const TX *__restrict__ x, int n, int64_t ldx, bool wide,
                     const int32_t *__restrict__ offsets, Fp4Matrix w, int d_in, void *__restrict__ y,
-                    int yt, int64_t ldy, int parts, int shares, int panel)
+                    int yt, int64_t ldy, int part_log, int shares, int panel)
 {
     using namespace gv;
     constexpr int P = Pieces<TX>::n, kPass = NT * 8 / P;  // rows of x per pass: P columns each
     constexpr int kBlocks = 32 / fp4_block(FMT);     // blocks of a lane's 32 elements
     // x: a word's 8 columns by 4 lanes t in the order of the lanes that read them
-    extern __shared__ uint4 xs[];  // [panel][NT][4 words][columns][4 lanes t]
+    extern __shared__ uint4 xs[];  // [panel][NT][4 words][8 columns][4 lanes t]
     __shared__ float sums[kWarps][NT * 8][kSumPitch];
     // the multiplier of each scale byte (83 us where computing them takes 87, 16 rows over 8 experts
     // 4096 -> 14336; 37 and 39, 10 rows in 32 bits)
@@ -208,12 +218,9 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
     const uint32_t tail = left_blocks >= kBlocks ? 0xFFFFu : (left_blocks == 1 ? 0xFFu : 0u);
     const int64_t first = static_cast<int64_t>(e) * d_out;
     const float scale = (w.t == nullptr ? 1.f : __ldg(w.t + e)) * kUnshift<FMT>;
-    // a round: kWarps / parts tiles of this CTA, every clusters-th of the matrix
-    const int slots = kWarps / parts, slot = warp / parts, part = warp % parts;
-    const int rounds = ((tiles - cluster + clusters - 1) / clusters + slots - 1) / slots;
+    const int own = (chunks + shares - 1) / shares;  // chunks of the cluster's largest share
+    const int count = (tiles - cluster + clusters - 1) / clusters;  // tiles: every clusters-th
     const bool once = c_end - c_begin <= panel;  // x fits at once
-    // columns kept of each tile: one tile of few rows keeps only theirs
-    const int columns = NT > 1 ? 8 : min(kPass, rows.y - rows.x) * P;
 
     for (int b0 = rows.x; b0 < rows.y; b0 += kPass) {
         const int tokens = min(kPass, rows.y - b0);
@@ -227,7 +234,7 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
                     const int at = token * P + p;  // column of the pass
-                    xs[(((c * NT + at / 8) * 4 + (q >> 2)) * columns + at % 8) * 4 + (q & 3)] = col[p];
+                    xs[((c * NT + at / 8) * 4 + (q >> 2)) * 32 + at % 8 * 4 + (q & 3)] = col[p];
                 }
             }
         };
@@ -246,12 +253,20 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                 q.s1 = __ldg(scales1 + ahead * 4);
             }
         };
-        auto tile_of = [&](int round) { return cluster + (round * slots + slot) * clusters; };
-        // the first chunks of this warp's part of chunks p0 .. p1 - 1 of a tile
-        auto begin = [&](int tile, int p0, int p1) {
+        // this warp's tile of a round that begins at the CTA's tile `done`, and its part of chunks
+        // p0 .. p1 - 1
+        auto tile_of = [&](int done, int log) { return cluster + (done + (warp >> log)) * clusters; };
+        auto part_of = [&](int log, int p0, int p1) {
+            const int part = warp & ((1 << log) - 1);
+            return make_int2(p0 + (part * (p1 - p0) >> log), p0 + ((part + 1) * (p1 - p0) >> log));
+        };
+        // the first chunks of it
+        auto begin = [&](int done, int log, int p0, int p1) {
+            const int tile = tile_of(done, log);
             if (tile >= tiles)
                 return;
-            const int w_begin = p0 + part * (p1 - p0) / parts, w_end = p0 + (part + 1) * (p1 - p0) / parts;
+            const int2 part = part_of(log, p0, p1);
+            const int w_begin = part.x, w_end = part.y;
             // outputs behind the last (nobody writes their sums) repeat it
             const int64_t r0 = first + min(tile * kRows + g, d_out - 1);
             const int64_t r1 = first + min(tile * kRows + g + 8, d_out - 1);
@@ -263,15 +278,19 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
             for (int u = 0; u < kAhead; ++u)
                 fetch(ring[u], u, w_end - w_begin - u);
         };
+        int log = gemv_round_log(part_log, count, own);
         if (once)
-            begin(tile_of(0), c_begin, c_end);  // its loads run while x is written
+            begin(0, log, c_begin, c_end);  // its loads run while x is written
         __syncthreads();  // the last pass has read x; the multipliers are written
         if (once) {
             stage(c_begin, c_end);
             __syncthreads();
         }
-        for (int round = 0; round < rounds; ++round) {
-            const bool mine = tile_of(round) < tiles;
+        for (int done = 0, slots, next; done < count; done += slots, log = next) {
+            const int parts = 1 << log;
+            slots = kWarps >> log;
+            next = gemv_round_log(part_log, count - done - slots, own);
+            const bool mine = tile_of(done, log) < tiles;
             float acc[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -284,13 +303,14 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                     __syncthreads();
                     stage(p0, p1);
                     __syncthreads();
-                    begin(tile_of(round), p0, p1);
+                    begin(done, log, p0, p1);
                 }
                 if (!mine)
                     continue;
-                const int w_begin = p0 + part * (p1 - p0) / parts, w_end = p0 + (part + 1) * (p1 - p0) / parts;
-                // a column that no row has repeats another: nobody reads its sums
-                const uint4 *xc = xs + (w_begin - p0) * (NT * 16) * columns + min(g, columns - 1) * 4 + t;
+                const int2 part = part_of(log, p0, p1);
+                const int w_begin = part.x, w_end = part.y;
+                // (the columns behind the last row's hold anything: nobody reads their sums)
+                const uint4 *xc = xs + (w_begin - p0) * (NT * 128) + lane;
                 for (int c0 = w_begin; c0 < w_end; c0 += kAhead) {
 #pragma unroll
                     for (int u = 0; u < kAhead; ++u) {
@@ -327,12 +347,12 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                const uint4 v = xc[(nt * 16 + j * 4) * columns];
+                                const uint4 v = xc[nt * 128 + j * 32];
                                 mma_bf16(acc[nt], lo, v.x, v.y);
                                 mma_bf16(acc[nt], hi, v.z, v.w);
                             }
                         }
-                        xc += NT * 16 * columns;
+                        xc += NT * 128;
                         fetch(q, u + kAhead, w_end - c - kAhead);
                     }
                     codes0 += kAhead * 64;
@@ -341,8 +361,8 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                     scales1 += kAhead * 4 * kBlocks;
                 }
             }
-            if (once && round + 1 < rounds)  // the next tile's loads run while this one's sums are added
-                begin(tile_of(round + 1), c_begin, c_end);
+            if (once && done + slots < count)  // the next tile's loads run while this one's sums are added
+                begin(done + slots, next, c_begin, c_end);
             if (mine) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -363,7 +383,7 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                 return sum;
             };
             auto put = [&](int k, int b, int r, float sum) {
-                const int j = (cluster + (round * slots + k) * clusters) * kRows + r;
+                const int j = (cluster + (done + k) * clusters) * kRows + r;
                 if (b0 + b >= rows.y || j >= d_out)
                     return;
                 sum *= scale;
@@ -432,15 +452,15 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // How K is shared: by `shares` CTAs of a cluster (less of x for each to write) and `parts`
-    // warps of a CTA (fewer idle warps in the last round). The least time, in units of 6.5 ns, fitted
-    // to 15 sizes at all shares and parts, two CTAs an SM (it picks the fastest at each or one within
-    // 1% of it): a chunk of a column of x staged, a chunk of a tile, and a round's fixed costs,
-    // which are larger where a cluster's CTAs wait for one another.
+    // How K is shared: by `shares` CTAs of a cluster (less of x for each to write) and 2^`part_log`
+    // warps of a CTA. The least time, in units of 6.5 ns, fitted to 15 sizes at all shares and parts,
+    // two CTAs an SM (it picks the fastest at each or one within 1% of it): a chunk of a column of x
+    // staged, a chunk of a tile, and a round's fixed costs, which are larger where a cluster's
+    // CTAs wait for one another.
     constexpr int64_t kWork = 62 + 13 * NT, kRound = 390, kClusterRound = 530;
     const int64_t stage = min((n + experts - 1) / experts, int64_t(NT * 8 / Pieces<TX>::n)) * Pieces<TX>::n * 4;
     static std::atomic<int> resident[4];  // clusters that run at once, by their size
-    int shares = 1, parts = 1;
+    int shares = 1, part_log = 0;
     int64_t clusters = 1, best = INT64_MAX;
     for (int i = 0, c = 1; c <= kMaxShares && (c == 1 || chunks >= c * 2); ++i, c *= 2) {
         int room = resident[i].load(std::memory_order_relaxed);
@@ -460,14 +480,16 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
         }
         const int64_t own = (chunks + c - 1) / c, m = max(int64_t(1), min(tiles, room / busy));
         const int64_t per_cta = (tiles + m - 1) / m, waves = (m * busy + room - 1) / room;
-        for (int k = 1; k <= kWarps && (k == 1 || own >= k * 2); k *= 2) {
-            const int64_t rounds = (per_cta * k + kWarps - 1) / kWarps;
-            const int64_t stagings = own * kChunkBytes > kXBytes ? rounds : 1;
-            const int64_t cost = waves * (stagings * own * stage +
-                                          rounds * ((own + k - 1) / k * kWork +
-                                                    (c > 1 ? kClusterRound : kRound)));
+        for (int k = 0; k < 4 && (k == 0 || own >= 2 << k); ++k) {
+            const int64_t whole = per_cta / (kWarps >> k), left = per_cta % (kWarps >> k);
+            const int last = gemv_round_log(k, static_cast<int>(left), static_cast<int>(own));
+            const int64_t rounds = whole + (left > 0), stagings = own * kChunkBytes > kXBytes ? rounds : 1;
+            const int64_t work = whole * ((own + (1 << k) - 1) >> k) +
+                                 (left > 0 ? (own + (1 << last) - 1) >> last : 0);
+            const int64_t cost = waves * (stagings * own * stage + work * kWork +
+                                          rounds * (c > 1 ? kClusterRound : kRound));
             if (cost < best)
-                best = cost, shares = c, parts = k, clusters = m;
+                best = cost, shares = c, part_log = k, clusters = m;
         }
     }
     const int64_t panel = min((chunks + shares - 1) / shares, kXBytes / kChunkBytes);
@@ -476,7 +498,7 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
     cfg.dynamicSmemBytes = static_cast<size_t>(panel * kChunkBytes);
     KernelTimer timer("lnq_fp4_gemv", s);
     e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const TX *>(x), n, ldx, wide, offsets, w,
-                           static_cast<int>(d_in), y, yt, ldy, parts, shares, static_cast<int>(panel));
+                           static_cast<int>(d_in), y, yt, ldy, part_log, shares, static_cast<int>(panel));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
