@@ -259,6 +259,28 @@ def test_gemv(lnq, fmt, dtype, n, d_in, d_out, exact):
         check_product(y, f64(x), w, 1.0 if t is None else float(np.float32(t)), exact)
 
 
+@pytest.mark.parametrize("fmt,dtype,n,d_in,d_out,experts", [
+    (MX, torch.float32, 5, 8200, 5001, 1), (NV, torch.bfloat16, 1, 4100, 9001, 1),
+    (NV, torch.float16, 20, 5000, 2600, 1), (MX, torch.bfloat16, 9, 12000, 1500, 1),
+    (NV, torch.bfloat16, 7, 2100, 4700, 3), (MX, torch.float32, 11, 900, 4700, 3)])
+def test_gemv_many_tiles(lnq, fmt, dtype, n, d_in, d_out, experts):
+    """Several rounds of tiles to a CTA, the last one not full; K shared among warps and CTAs."""
+    rng = _rng(n, d_in, d_out)
+    x = _operand(rng, n, d_in, dtype, True)
+    codes, scales = ref.random_stored(rng, (experts, d_out), d_in, fmt, True)
+    if experts == 1:
+        y = lnq.lnq_fp4_gemv(x, dev(codes[0]), dev(scales[0]), fmt, dtype=torch.float32)
+        ends = [0, n]
+    else:
+        ends = [0, 4, 4, n]
+        y = lnq.lnq_fp4_grouped_gemv(x, dev(np.array(ends, np.int32)), dev(codes), dev(scales), fmt,
+                                     dtype=torch.float32)
+    for e in range(experts):
+        rows = slice(ends[e], ends[e + 1])
+        if ends[e + 1] > ends[e]:
+            check_product(y[rows], f64(x)[rows], ref.values(codes[e], scales[e], d_in, fmt), exact=True)
+
+
 def test_gemv_strided(lnq):
     rng = _rng(9)
     for dtype in TYPES:
