@@ -6,7 +6,7 @@
 // Bound: HBM, the codes and scales read once (half a byte and 1/16 (NV) or 1/32 (MX) of a byte an
 // element); in practice the decoding, about 3.4 instructions an element (integer pipe 57% busy). One
 // B200: 16 rows over 8 experts 4096 -> 14336 73 us (3.6 TB/s of codes and scales), 1 x 4096 -> 14336
-// 14 us, 1 x 4096 -> 4096 7.4 us, 7 x 11008 -> 4101 in 32 bits 22 us.
+// 14 us, 1 x 4096 -> 4096 8.3 us, 7 x 11008 -> 4101 in 32 bits 22 us.
 //
 // The products run on mma.sync m16n8k16 in bf16 with 32-bit sums: with at most a few rows the
 // work is decoding weights, and the instruction takes them straight from registers, where
