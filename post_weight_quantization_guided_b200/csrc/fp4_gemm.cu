@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_remote(ready_leader + static_cast<uint32_t>(slot * 8));
+                mbar_arrive_smem_written(ready_leader + static_cast<uint32_t>(slot * 8));
             advance();
             advance();
             fetch();
@@ -437,14 +437,11 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                         sts_words4(st + atom * kAtom + lane * 16, v[g * 4][k], v[g * 4 + 1][k],
                                    v[g * 4 + 2][k], v[g * 4 + 3][k]);
                     }
-                // After the fence every lane's stores are in this CTA's shared memory, where the
-                // tensor core reads them. The arrival is sent behind it, without a release at
-                // cluster scope: that would also wait for all other writes of this SM (the
-                // epilogue's stores to global memory), at 0.3 us a step.
+                // The leader's thread has the tensor core of this CTA read these stores.
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_remote(ready_leader + static_cast<uint32_t>(at_slot * 8));
+                    mbar_arrive_smem_written(ready_leader + static_cast<uint32_t>(at_slot * 8));
             }
         }
     } else if (warp == kMmaWarp) {
@@ -546,8 +543,8 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 tmem_ld_fence(v[c]);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)  // what it orders are TMEM reads: no release at cluster scope
-                mbar_arrive_remote(tempty_leader + static_cast<uint32_t>(acc * 8));
+            if (lane == 0)
+                mbar_arrive_tmem_read(tempty_leader + static_cast<uint32_t>(acc * 8));
             if (p.split > 1) {
                 // this pair's share of the sums, [row][128 outputs], over the finished stages
                 float *sums = reinterpret_cast<float *>(smem);
