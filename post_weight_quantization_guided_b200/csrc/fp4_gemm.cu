@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     uint64_t *tempty = tfull + T::kAcc;              // accumulator read (leader's: both CTAs')
     uint64_t *drain = tempty + T::kAcc;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *loaded = drain + 2;  // 1 + stages of codes this CTA loaded, once its loads are over
     int *lim = reinterpret_cast<int *>(tmem_holder + 4);  // [experts + 1] group boundaries
     int *pre = lim + T::kLimInts;                         // [experts + 1] row tiles before group e
 
@@ -174,8 +175,11 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     const int kb0 = part * steps / p.split * 2;
     const int kb1 = min((part + 1) * steps / p.split * 2, p.nk);
     DeviceErr err{g_fp4_error, p.limit};
+    // for what ends by itself, or with a wait of `limit` elsewhere in the cluster
+    const long long last_limit = (p.limit < (1LL << 62) ? p.limit : 1LL << 62) + kDrainLimit;
 
     if (threadIdx.x == 32) {
+        *loaded = 0u;
         for (int s = 0; s < T::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -250,10 +254,28 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
         if (lane == 0) {
             int64_t tile = first, sf_tile = p.sf_tma ? first : num_tiles;
             int kb = kb0, sf_kb = kb0, stage = 0, slot = 0;
-            uint32_t par = 1u, sf_par = 1u, used = 0u, sf_used = 0u;
+            uint32_t par = 1u, sf_par = 1u, sf_used = 0u;
             Fp4TileAt at = {0, 0, 0, 0}, sf_at = {0, 0, 0, 0};
             if (first < num_tiles)
                 at = sf_at = tile_at<BN>(first, p, lim, pre);
+            uint64_t count = 0u;  // stages of codes loaded
+            auto load_stage = [&]() {
+                uint8_t *st = smem + stage * T::kStageBytes;
+                if (cr == 0)
+                    mbar_arrive_expect_tx(&full[stage], 2 * T::kStageBytes);
+                const uint32_t fb = cluster_addr(&full[stage], leader);
+                tma_load_2d_pair(st, &wmap, fb, kb * 128, at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM);
+                tma_load_2d_pair(st + T::kABytes, &amap, fb, kb * 128, at.b0 + static_cast<int>(cr) * (BN / 2));
+                ++count;
+                stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                par ^= stage == 0 ? 1u : 0u;
+                if (++kb == kb1) {
+                    kb = kb0;
+                    tile += step;
+                    if (tile < num_tiles)
+                        at = tile_at<BN>(tile, p, lim, pre);
+                }
+            };
             long long since = clock64();
             while (tile < num_tiles || sf_tile < num_tiles) {
                 bool moved = false;
@@ -276,23 +298,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                     moved = true;
                 }
                 if (tile < num_tiles && mbar_test(&empty[stage], par)) {
-                    uint8_t *st = smem + stage * T::kStageBytes;
-                    if (cr == 0)
-                        mbar_arrive_expect_tx(&full[stage], 2 * T::kStageBytes);
-                    const uint32_t fb = cluster_addr(&full[stage], leader);
-                    tma_load_2d_pair(st, &wmap, fb, kb * 128,
-                                     at.e * p.d_out + at.j0 + static_cast<int>(cr) * BM);
-                    tma_load_2d_pair(st + T::kABytes, &amap, fb, kb * 128,
-                                     at.b0 + static_cast<int>(cr) * (BN / 2));
-                    used |= 1u << stage;
-                    stage = stage + 1 == T::kStages ? 0 : stage + 1;
-                    par ^= stage == 0 ? 1u : 0u;
-                    if (++kb == kb1) {
-                        kb = kb0;
-                        tile += step;
-                        if (tile < num_tiles)
-                            at = tile_at<BN>(tile, p, lim, pre);
-                    }
+                    load_stage();
                     moved = true;
                 }
                 if (moved) {
@@ -302,22 +308,23 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                     break;
                 }
             }
-            if (tile < num_tiles || sf_tile < num_tiles) {
-                // Gave up: let this CTA's copies land. The codes' are counted on the leader's
-                // barriers, so the leader waits for the last fill of each and its peer a fixed time.
-                for (int s = 0; s < kScaleRing; ++s)
-                    if ((sf_used >> s) & 1u)
-                        mbar_wait(&sf_raw[s], s < slot ? sf_par ^ 1u : sf_par, kDrainLimit);
-                if (cr == 0) {
-                    for (int s = 0; s < T::kStages; ++s)
-                        if ((used >> s) & 1u)
-                            mbar_wait(&full[s], s < stage ? par ^ 1u : par, 1LL << 22);
-                } else {
-                    const long long c0 = clock64();
-                    while (clock64() - c0 < (1LL << 22)) {
-                    }
-                }
+            // No copy may be in flight when this CTA exits, whichever thread of the pair gave up: all
+            // that was loaded is waited for here, which costs nothing where it is multiplied too.
+            // The codes of both CTAs are counted together, on the leader's barriers. So a CTA that
+            // gave up first loads the stages that its peer has loaded and it has not: the peer saw
+            // them empty, and so they are (one commit tells both).
+            st_release_cluster(loaded, count + 1u);
+            if (tile < num_tiles) {
+                const uint64_t theirs = wait_nonzero_cluster(cluster_addr(loaded, rank ^ 1u), last_limit);
+                while (count + 1u < theirs)
+                    load_stage();
             }
+            for (int s = 0; s < kScaleRing; ++s)
+                if ((sf_used >> s) & 1u)
+                    mbar_wait(&sf_raw[s], s < slot ? sf_par ^ 1u : sf_par, last_limit);
+            for (int s = 0; s < T::kStages && cr == 0; ++s)
+                if (static_cast<uint64_t>(s) < count)
+                    mbar_wait(&full[s], s < stage ? par ^ 1u : par, last_limit);
         }
     } else if ((warp == kScaleWarp || warp == kLoadWarp) && !p.sf_tma) {
         // ------------------------------------------------------------------ scales without TMA
@@ -501,9 +508,12 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 acc = acc + 1 == T::kAcc ? 0 : acc + 1;
                 aph ^= acc == 0 ? 1u : 0u;
             }
-            // every MMA of this thread has completed once `drain` flips
-            umma_commit_pair(drain, static_cast<uint16_t>(1u << leader));
-            mbar_wait(drain, 0, kDrainLimit);
+            // every MMA of this thread has completed, and its commits have arrived, once `drain`
+            // flips
+            umma_commit_pair(drain, pair_mask);
+            mbar_wait(drain, 0, last_limit);
+        } else if (cr != 0 && lane == 0) {
+            mbar_wait(drain, 0, last_limit);
         }
     } else {
         // ------------------------------------------------------------------ epilogue
@@ -580,7 +590,8 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
 
     if (p.split > 1) {
         // One tile per cluster. Each pair adds and writes its share of the rows, over the pairs
-        // in order.
+        // in order. (After a wait that gave up they may add anything: nothing is being copied to the
+        // stages any more, and the call is reported.)
         __syncwarp();
         cluster_sync();
         const Fp4TileAt at = tile_at<BN>(first, p, lim, pre);

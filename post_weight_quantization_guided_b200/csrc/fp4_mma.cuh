@@ -47,6 +47,22 @@ __device__ __forceinline__ void mbar_arrive_tmem_read(uint32_t bar_cluster_addr)
                  : "memory");
 }
 
+// A word of this CTA's shared memory that another CTA of the cluster waits for: the store, and the
+// wait until it is not zero (for at most `limit` SM cycles; 0 if it gave up).
+__device__ __forceinline__ void st_release_cluster(uint64_t *p, uint64_t v)
+{
+    asm volatile("st.release.cluster.shared::cta.u64 [%0], %1;" ::"r"(smem_u32(p)), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint64_t wait_nonzero_cluster(uint32_t cluster_address, long long limit)
+{
+    const long long t0 = clock64();
+    uint64_t v;
+    do {
+        asm volatile("ld.acquire.cluster.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_address) : "memory");
+    } while (v == 0u && clock64() - t0 < limit);
+    return v;
+}
+
 // N (1 or 2) consecutive words of global memory.
 template <int N>
 __device__ __forceinline__ void ldg_words(uint32_t *v, const uint8_t *src)
