@@ -126,9 +126,14 @@ LNQ_API lnq_status lnq_fp4_grouped_gemm(const uint8_t *a_codes, const uint8_t *a
                                         int64_t d_in, lnq_fp4_format fmt, void *y, lnq_dtype yt,
                                         int64_t ldy, lnq_stream_t stream);
 
-/* Synchronises `stream` and reports whether a bounded wait inside an lnq_fp4_* product on the
- * current device has given up since the last such report (LNQ_ERR_TIMEOUT: the results of the
- * calls since then are incomplete), and clears the report. */
+/* Synchronises `stream` and reports whether a bounded wait inside an lnq_fp4_* product has given up
+ * (LNQ_ERR_TIMEOUT: the results of the calls concerned are incomplete), on the current device:
+ *   a stream: in a product called on it, or in one captured into a graph, wherever the graph ran;
+ *   the default stream (NULL): in any product of the device;
+ * each since the stream's last report, or since the library was loaded. Every stream has reports of
+ * its own, and one stream's takes nothing from another's; callers that share a stream share them.
+ * Streams beyond the first thousand may share a count, and then both report; a stream that got the
+ * handle of a destroyed one also got its reports. */
 LNQ_API lnq_status lnq_fp4_check(lnq_stream_t stream);
 
 #ifdef __cplusplus

@@ -94,8 +94,18 @@ cudaError_t fp4_gemv_launch(const void *x, int xt, int64_t n, int64_t ldx, const
 cudaError_t fp4_gemm_launch(const Fp4Matrix &a, const int32_t *offsets, int64_t experts,
                             const Fp4Matrix &w, int64_t d_in, int fmt, void *y, int yt,
                             int64_t ldy, long long wait_limit, int num_sms, cudaStream_t s);
-// Flags raised by the products' bounded waits on the current device (see lnq_fp4_check).
-cudaError_t fp4_take_error_flags(uint32_t *flags, cudaStream_t s);
+// The products' bounded waits that gave up on a device since the library was loaded (modulo 2^32): of
+// products on one stream (and on those that share its slot), of products captured into graphs, of all.
+struct Fp4GiveUps {
+    uint32_t own, captured, all;
+};
+constexpr int kFp4ReportSlots = 1024;
+// The counts as they are once `s` has been synchronised, on the current device.
+cudaError_t fp4_give_ups(Fp4GiveUps *counts, cudaStream_t s);
+// fp4_report.cu: the slot of a stream's count; whether the counts hold something this stream has not
+// been told of, and that it has been told now (the default stream: of all of the device's).
+int fp4_report_slot(cudaStream_t s);
+bool fp4_report_news(int device, cudaStream_t s, const Fp4GiveUps &now);
 
 // api.cu
 int device_sm_count();

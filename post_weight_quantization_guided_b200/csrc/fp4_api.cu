@@ -170,10 +170,12 @@ lnq_status lnq_fp4_grouped_gemm(const uint8_t *a_codes, const uint8_t *a_scales,
 
 lnq_status lnq_fp4_check(lnq_stream_t stream)
 {
-    uint32_t flags = 0u;
-    if (fp4_take_error_flags(&flags, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Fp4GiveUps counts = {0u, 0u, 0u};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || fp4_give_ups(&counts, s) != cudaSuccess)
         return LNQ_ERR_CUDA;
-    return flags != 0u ? LNQ_ERR_TIMEOUT : LNQ_OK;
+    return fp4_report_news(device, s, counts) ? LNQ_ERR_TIMEOUT : LNQ_OK;
 }
 
 }  // extern "C"

@@ -41,7 +41,16 @@
 
 namespace lnq {
 
-__device__ uint32_t g_fp4_error[2];
+// Waits that gave up: by the slot of the product's stream, [kCapturedSlot] of products captured into
+// a graph, which runs on any stream, and [kAllSlot] of all.
+constexpr int kCapturedSlot = kFp4ReportSlots, kAllSlot = kFp4ReportSlots + 1;
+__device__ uint32_t g_fp4_gave_up[kFp4ReportSlots + 2];
+
+__device__ __forceinline__ void give_up(int slot)
+{
+    atomicAdd(&g_fp4_gave_up[slot], 1u);
+    atomicAdd(&g_fp4_gave_up[kAllSlot], 1u);
+}
 
 namespace f4 {
 constexpr int BM = 128, PM = 256;       // outputs of a CTA, of a pair
@@ -98,6 +107,7 @@ struct Fp4GemmParams {
     int mt;                // output tiles of one matrix
     int split;             // pairs that share a tile's K
     int sf_tma;            // scales by TMA: rows are multiples of 16 bytes
+    int report;            // where a wait that gives up is counted
     long long limit;
 };
 
@@ -174,7 +184,6 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     const int steps = (p.nk + 1) / 2;  // of two stages
     const int kb0 = part * steps / p.split * 2;
     const int kb1 = min((part + 1) * steps / p.split * 2, p.nk);
-    DeviceErr err{g_fp4_error, p.limit};
     // for what ends by itself, or with a wait of `limit` elsewhere in the cluster
     const long long last_limit = (p.limit < (1LL << 62) ? p.limit : 1LL << 62) + kDrainLimit;
 
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 if (moved) {
                     since = clock64();
                 } else if (clock64() - since >= p.limit) {
-                    raise_error(err, kErrTimeout, 1);
+                    give_up(p.report);
                     break;
                 }
             }
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
         while (tile < num_tiles) {
             if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[slot], phase, p.limit))) {
                 if (lane == 0)
-                    raise_error(err, kErrTimeout, 2);
+                    give_up(p.report);
                 break;
             }
             const uint32_t st = smem_u32(sf) + static_cast<uint32_t>(slot * T::kStepBytes);
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                     continue;
                 if (!__all_sync(0xffffffffu, mbar_wait(&sf_raw[at_slot], at_phase, p.limit))) {
                     if (lane == 0)
-                        raise_error(err, kErrTimeout, 3);
+                        give_up(p.report);
                     ok = false;
                     break;
                 }
@@ -460,7 +469,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
             bool ok = true;
             for (int64_t tile = first; tile < num_tiles && ok; tile += step) {
                 if (!mbar_wait_cluster(&tempty[acc], aph, p.limit)) {
-                    raise_error(err, kErrTimeout, 4);
+                    give_up(p.report);
                     ok = false;
                     break;
                 }
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                     const int h = (kb - kb0) & 1;  // stage of the step
                     if ((h == 0 && !mbar_wait_cluster(&sf_ready[slot], sph, p.limit)) ||
                         !mbar_wait(&full[stage], fph, p.limit)) {
-                        raise_error(err, kErrTimeout, 5);
+                        give_up(p.report);
                         ok = false;
                         break;
                     }
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) {
                 if (lane == 0)
-                    raise_error(err, kErrTimeout, 6);
+                    give_up(p.report);
                 break;
             }
             __syncwarp();
@@ -752,6 +761,10 @@ cudaError_t fp4_gemm_launch(const Fp4Matrix &a, const int32_t *offsets, int64_t 
     p.scale_pitch = static_cast<int>(fp4_scale_pitch(d_in, fmt));
     p.mt = static_cast<int>((w.rows + f4::PM - 1) / f4::PM);
     p.limit = wait_limit;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess)
+        return cudaErrorInvalidValue;
+    p.report = capture == cudaStreamCaptureStatusNone ? fp4_report_slot(s) : kCapturedSlot;
     // an upper bound of the row tiles where the groups are not known here
     auto tiles_of = [&](int rows) {
         return p.mt * (offsets == nullptr ? (a.rows + rows - 1) / rows
@@ -807,19 +820,18 @@ cudaError_t fp4_gemm_launch(const Fp4Matrix &a, const int32_t *offsets, int64_t 
     }
 }
 
-cudaError_t fp4_take_error_flags(uint32_t *flags, cudaStream_t s)
+cudaError_t fp4_give_ups(Fp4GiveUps *counts, cudaStream_t s)
 {
-    static const uint32_t zero[2] = {0u, 0u};
-    cudaError_t e = cudaMemcpyFromSymbolAsync(flags, g_fp4_error, sizeof(uint32_t), 0,
-                                              cudaMemcpyDeviceToHost, s);
+    auto read = [&](uint32_t *to, int slot) {
+        return cudaMemcpyFromSymbolAsync(to, g_fp4_gave_up, sizeof(uint32_t), slot * sizeof(uint32_t),
+                                         cudaMemcpyDeviceToHost, s);
+    };
+    cudaError_t e = read(&counts->own, fp4_report_slot(s));
     if (e == cudaSuccess)
-        e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && flags[0] != 0u) {
-        e = cudaMemcpyToSymbolAsync(g_fp4_error, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess)
-            e = cudaStreamSynchronize(s);
-    }
-    return e;
+        e = read(&counts->captured, kCapturedSlot);
+    if (e == cudaSuccess)
+        e = read(&counts->all, kAllSlot);
+    return e != cudaSuccess ? e : cudaStreamSynchronize(s);
 }
 
 }  // namespace lnq

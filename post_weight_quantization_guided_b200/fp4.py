@@ -306,8 +306,11 @@ def lnq_fp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, offsets:
 
 
 def lnq_fp4_check(device=None, stream=None) -> int:
-    """Synchronises the stream and returns LNQ_OK or LNQ_ERR_TIMEOUT (see include/lnq_fp4.h) for
-    the products run on `device` (the current one by default)."""
+    """Synchronises the stream (the current one by default) and returns LNQ_OK, or LNQ_ERR_TIMEOUT
+    if a product on it, or for the default stream any product of `device` (the stream's or the
+    current one by default), has given up since its last report (see include/lnq_fp4.h)."""
+    if device is None and stream is not None:
+        device = stream.device
     with torch.cuda.device(device):
         if stream is None:
             stream = torch.cuda.current_stream()

@@ -82,3 +82,88 @@ def test_the_grouped_product_behind_one_that_gave_up_is_whole(lnq, fmt):
         y = lnq.lnq_fp4_grouped_gemm(a, sa, o, w, sw, 1032, fmt, dtype=torch.float32)
         assert lnq.lnq_fp4_check() in ((TIMEOUT,) if limit == 0 else (0, TIMEOUT))
         assert torch.equal(y, want)
+
+
+# --------------------------------------------------------------------------- who is told of it
+
+def _gives_up(lnq, args, stream=None):
+    lnq.lnq_set_wait_limit(0)
+    try:
+        return lnq.lnq_fp4_gemm(*args, 1024, MX, stream=stream)
+    finally:
+        lnq.lnq_set_wait_limit(-1)
+
+
+@pytest.fixture()
+def args(lnq):
+    a = operands(MX, 20, 1024, 300)[:4]
+    torch.cuda.synchronize()
+    yield a
+    lnq.lnq_fp4_check()  # the default stream has been told of all
+
+
+def test_each_of_two_streams_has_its_own_report(lnq, args):
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, other):
+        lnq.lnq_fp4_check(stream=st)
+    _gives_up(lnq, args, s)
+    lnq.lnq_fp4_gemm(*args, 1024, MX, stream=other)
+    assert lnq.lnq_fp4_check(stream=other) == 0         # its product is whole, and it takes
+    assert lnq.lnq_fp4_check(stream=s) == TIMEOUT       # nothing from the other stream's report
+    assert lnq.lnq_fp4_check(stream=s) == 0
+    assert lnq.lnq_fp4_check() == TIMEOUT               # the default stream's: of the device
+    assert lnq.lnq_fp4_check() == 0
+
+
+def test_a_report_on_the_default_stream_takes_none_from_a_stream(lnq, args):
+    s = torch.cuda.Stream()
+    lnq.lnq_fp4_check(stream=s)
+    _gives_up(lnq, args, s)
+    s.synchronize()
+    assert lnq.lnq_fp4_check() == TIMEOUT
+    assert lnq.lnq_fp4_check(stream=s) == TIMEOUT
+    _gives_up(lnq, args)
+    assert lnq.lnq_fp4_check(stream=s) == 0             # called on the default stream
+    assert lnq.lnq_fp4_check() == TIMEOUT
+
+
+def test_a_captured_product_is_reported_where_it_runs(lnq, args):
+    graph, s, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    lnq.lnq_set_wait_limit(0)
+    try:
+        with torch.cuda.graph(graph):
+            lnq.lnq_fp4_gemm(*args, 1024, MX)
+    finally:
+        lnq.lnq_set_wait_limit(-1)
+    for st in (s, other, None):
+        lnq.lnq_fp4_check(stream=st)
+        assert lnq.lnq_fp4_check(stream=st) == 0
+    with torch.cuda.stream(s):
+        graph.replay()
+    for st in (s, other, None):
+        assert lnq.lnq_fp4_check(stream=st) == TIMEOUT
+        assert lnq.lnq_fp4_check(stream=st) == 0
+
+
+def test_two_threads_check_while_one_products_give_up(lnq, args):
+    """One caller checks all the time; every give-up of the other is reported to the other."""
+    import threading
+    s, noisy = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, noisy):
+        lnq.lnq_fp4_check(stream=st)
+    stop, seen = threading.Event(), []
+
+    def watch():
+        while not stop.is_set():
+            seen.append(lnq.lnq_fp4_check(stream=noisy))
+
+    th = threading.Thread(target=watch)
+    th.start()
+    try:
+        for _ in range(50):
+            _gives_up(lnq, args, s)
+            assert lnq.lnq_fp4_check(stream=s) == TIMEOUT
+    finally:
+        stop.set()
+        th.join()
+    assert seen and not any(seen)
