@@ -3,6 +3,10 @@
 Argument marshalling only: every step of the path runs in the CUDA library. PyTorch supplies
 device memory and the current stream. If the library is missing, the functions raise; there is no
 fallback of any kind.
+
+With `stream=` a call runs on that stream, and what it allocates is that stream's memory. The caller
+sees to it that the inputs are written before and not overwritten or freed meanwhile, and that
+whoever reads the outputs on another stream waits.
 """
 from __future__ import annotations
 
@@ -126,10 +130,22 @@ def _need(t: torch.Tensor, dtype, shape, name):
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def workspace(op: int, n=0, d_in=0, d_out=0, groups=1, m=2, device="cuda") -> torch.Tensor:
-    """A device workspace of the size the library asks for (torch's allocator aligns to 512 B)."""
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor from the memory of the stream that the call runs on (None: the
+    current one). A block of another stream's memory might still be in use there, and this tensor's
+    block would go back to that stream while the call still runs on its own."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def workspace(op: int, n=0, d_in=0, d_out=0, groups=1, m=2, device="cuda",
+              stream=None) -> torch.Tensor:
+    """A device workspace of the size the library asks for (torch's allocator aligns to 512 B), for
+    calls on `stream` (the current one by default)."""
     size = lnq_workspace_size(op, n, d_in, d_out, groups, m)
-    return torch.empty(max(size, 256), dtype=torch.uint8, device=device)
+    return _empty(max(size, 256), torch.uint8, device, stream)
 
 
 def _check(status: int, where: str):
@@ -146,10 +162,11 @@ def lnq_build_fisher(X: torch.Tensor, G: Optional[torch.Tensor], groups: int, al
     if G is not None:
         _need(G, torch.bfloat16, (n, d_out), "G")
     if F is None:
-        F = torch.empty((groups, d_in, d_in), dtype=torch.float32, device=X.device)
+        F = _empty((groups, d_in, d_in), torch.float32, X.device, stream)
     _need(F, torch.float32, (groups, d_in, d_in), "F")
     if ws is None:
-        ws = workspace(LNQ_OP_BUILD_FISHER, n, d_in, d_out, groups, device=X.device)
+        ws = workspace(LNQ_OP_BUILD_FISHER, n, d_in, d_out, groups, device=X.device,
+                       stream=stream)
     _check(lib().lnq_build_fisher(_ptr(X), _ptr(G), n, d_in, d_out, groups, alpha, _ptr(F),
                                   _ptr(ws), ws.numel(), _stream(stream)), "lnq_build_fisher")
     return F
@@ -166,7 +183,7 @@ def lnq_build_fisher_noalloc(X: torch.Tensor, G: Optional[torch.Tensor], groups:
     if G is not None:
         _need(G, torch.bfloat16, (n, d_out), "G")
     if F is None:
-        F = torch.empty((groups, d_in, d_in), dtype=torch.float32, device=X.device)
+        F = _empty((groups, d_in, d_in), torch.float32, X.device, stream)
     _need(F, torch.float32, (groups, d_in, d_in), "F")
     _check(lib().lnq_build_fisher_noalloc(_ptr(X), _ptr(G), n, d_in, d_out, groups, alpha,
                                           _ptr(F), _stream(stream)), "lnq_build_fisher_noalloc")
@@ -185,13 +202,14 @@ def lnq_init_codebook(W: torch.Tensor, m: int, C: Optional[torch.Tensor] = None,
     d_out, d_in = W.shape
     _need(W, torch.float32, (d_out, d_in), "W")
     if C is None:
-        C = torch.empty((d_out, m), dtype=torch.float32, device=W.device)
+        C = _empty((d_out, m), torch.float32, W.device, stream)
     if Q is None:
-        Q = torch.empty((d_out, d_in), dtype=torch.uint8, device=W.device)
+        Q = _empty((d_out, d_in), torch.uint8, W.device, stream)
     _need(C, torch.float32, (d_out, m), "C")
     _need(Q, torch.uint8, (d_out, d_in), "Q")
     if ws is None:
-        ws = workspace(LNQ_OP_INIT_CODEBOOK, 0, d_in, d_out, 1, m, device=W.device)
+        ws = workspace(LNQ_OP_INIT_CODEBOOK, 0, d_in, d_out, 1, m, device=W.device,
+                       stream=stream)
     _check(lib().lnq_init_codebook(_ptr(W), d_out, d_in, m, _ptr(C), _ptr(Q), _ptr(ws),
                                    ws.numel(), _stream(stream)), "lnq_init_codebook")
     return C, Q
@@ -213,7 +231,8 @@ def lnq_quantize_rows(F: torch.Tensor, W: torch.Tensor, m: int, iters: int, C: t
     if row_status is not None:
         _need(row_status, torch.int32, (d_out,), "row_status")
     if ws is None:
-        ws = workspace(LNQ_OP_QUANTIZE_ROWS, 0, d_in, d_out, groups, m, device=W.device)
+        ws = workspace(LNQ_OP_QUANTIZE_ROWS, 0, d_in, d_out, groups, m, device=W.device,
+                       stream=stream)
     _check(lib().lnq_quantize_rows(_ptr(F), groups, _ptr(W), d_out, d_in, m, iters, _ptr(C),
                                    _ptr(Q), _ptr(J_out), _ptr(row_status), _ptr(ws), ws.numel(),
                                    _stream(stream)), "lnq_quantize_rows")
@@ -237,7 +256,8 @@ def lnq_ganq_rows(F: torch.Tensor, W: torch.Tensor, m: int, iters: int, C: torch
     if row_status is not None:
         _need(row_status, torch.int32, (d_out,), "row_status")
     if ws is None:
-        ws = workspace(LNQ_OP_GANQ_ROWS, 0, d_in, d_out, groups, m, device=W.device)
+        ws = workspace(LNQ_OP_GANQ_ROWS, 0, d_in, d_out, groups, m, device=W.device,
+                       stream=stream)
     _check(lib().lnq_ganq_rows(_ptr(F), groups, _ptr(W), d_out, d_in, m, iters, _ptr(C),
                                _ptr(Q), _ptr(J_out), _ptr(row_status), _ptr(ws), ws.numel(),
                                _stream(stream)), "lnq_ganq_rows")
@@ -274,9 +294,10 @@ def lnq_objective(F: torch.Tensor, W: torch.Tensor, C: torch.Tensor, Q: torch.Te
     _need(W, torch.float32, (d_out, d_in), "W")
     _need(Q, torch.uint8, (d_out, d_in), "Q")
     if J is None:
-        J = torch.empty(d_out, dtype=torch.float64, device=W.device)
+        J = _empty(d_out, torch.float64, W.device, stream)
     if ws is None:
-        ws = workspace(LNQ_OP_OBJECTIVE, 0, d_in, d_out, groups, m, device=W.device)
+        ws = workspace(LNQ_OP_OBJECTIVE, 0, d_in, d_out, groups, m, device=W.device,
+                       stream=stream)
     _check(lib().lnq_objective(_ptr(F), groups, _ptr(W), _ptr(C), _ptr(Q), d_out, d_in, m,
                                _ptr(J), _ptr(ws), ws.numel(), _stream(stream)), "lnq_objective")
     return J
@@ -316,7 +337,7 @@ def lnq_pack_codes(Q: torch.Tensor, bits: int, P: Optional[torch.Tensor] = None,
     _need(Q, torch.uint8, (d_out, d_in), "Q")
     words = lnq_packed_words(d_in, bits)
     if P is None:
-        P = torch.empty((d_out, words), dtype=torch.int32, device=Q.device)
+        P = _empty((d_out, words), torch.int32, Q.device, stream)
     _need(P, torch.int32, (d_out, words), "P")
     _check(lib().lnq_pack_codes(_ptr(Q), d_out, d_in, int(bits), _ptr(P), _stream(stream)),
            "lnq_pack_codes")
@@ -335,7 +356,7 @@ def lnq_lut_gemv(x: torch.Tensor, P: torch.Tensor, C: torch.Tensor, d_in: int,
     _need(C, torch.float32, (d_out, m), "C")
     _need(P, torch.int32, (d_out, lnq_packed_words(d_in, bits)), "P")
     if y is None:
-        y = torch.empty((nb, d_out), dtype=torch.float32, device=x.device)
+        y = _empty((nb, d_out), torch.float32, x.device, stream)
     _need(y, torch.float32, (nb, d_out), "y")
     _check(lib().lnq_lut_gemv(_ptr(x), nb, _ptr(P), _ptr(C), d_out, int(d_in), bits, _ptr(y),
                               _stream(stream)), "lnq_lut_gemv")

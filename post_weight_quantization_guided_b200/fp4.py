@@ -132,15 +132,19 @@ def _scale(t, count, fmt, name, device):
     return t.data_ptr()
 
 
-def _empty(like, shape, dtype):
-    """An uninitialised tensor on the device of `like`."""
-    return like.new_empty(shape, dtype=dtype)
+def _empty(like, shape, dtype, stream):
+    """An uninitialised tensor on the device of `like`, from the memory of the stream that the call
+    runs on (as in binding.py)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _output(y, like, shape, dtype):
+def _output(y, like, shape, dtype, stream):
     """(y, its type selector, its row pitch): the y given, or a new one of `dtype`."""
     if y is None:
-        return _empty(like, shape, _out_type(dtype)), _DTYPE[dtype], shape[1]
+        return _empty(like, shape, _out_type(dtype), stream), _DTYPE[dtype], shape[1]
     return y, *_dense(y, "y", shape, like.device)
 
 
@@ -169,7 +173,7 @@ def lnq_fp4_tensor_scale(x: torch.Tensor, t: Optional[torch.Tensor] = None,
     """t [1]: the matrix scale of LNQ_FP4_NV for x [rows][d], the largest finite |x| / 2688."""
     xt, ldx = _dense(x, "x")
     if t is None:
-        t = _empty(x, (1,), torch.float32)
+        t = _empty(x, (1,), torch.float32, stream)
     _need(t, torch.float32, (1,), "t", x.device)
     _call("lnq_fp4_tensor_scale", x.device, stream, x.data_ptr(), xt, x.shape[0], x.shape[1], ldx,
           t.data_ptr())
@@ -186,11 +190,11 @@ def lnq_fp4_quantize(x: torch.Tensor, fmt: int, tensor_scale: Optional[torch.Ten
     ts = _scale(tensor_scale, 1, fmt, "tensor_scale", dev)
     of_codes, of_scales = _pitches(d, fmt)
     if codes is None:
-        codes = _empty(x, (rows, of_codes), torch.uint8)
+        codes = _empty(x, (rows, of_codes), torch.uint8, stream)
     else:
         _need(codes, torch.uint8, (rows, of_codes), "codes", dev)
     if scales is None:
-        scales = _empty(x, (rows, of_scales), torch.uint8)
+        scales = _empty(x, (rows, of_scales), torch.uint8, stream)
     else:
         _need(scales, torch.uint8, (rows, of_scales), "scales", dev)
     _call("lnq_fp4_quantize", dev, stream, x.data_ptr(), xt, rows, d, ldx, fmt, ts,
@@ -207,7 +211,7 @@ def lnq_fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int, fmt: i
     rows = codes.shape[0]
     _codes(codes, scales, d, fmt, _INPUT, dev, (rows,))
     ts = _scale(tensor_scale, 1, fmt, "tensor_scale", dev)
-    y, yt, ldy = _output(y, codes, (rows, d), dtype)
+    y, yt, ldy = _output(y, codes, (rows, d), dtype, stream)
     _call("lnq_fp4_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, d, fmt, ts,
           y.data_ptr(), yt, ldy)
     return y
@@ -231,7 +235,7 @@ def _gemv(name, x, offsets, codes, scales, fmt, tensor_scale, y, dtype, stream):
     ts = _scale(tensor_scale, lead[0] if grouped else 1, fmt, "tensor_scale", dev)
     if grouped:
         _offsets(offsets, lead[0], dev)
-    y, yt, ldy = _output(y, codes, (n, lead[-1]), dtype or x.dtype)
+    y, yt, ldy = _output(y, codes, (n, lead[-1]), dtype or x.dtype, stream)
     group = (offsets.data_ptr(), lead[0]) if grouped else ()
     _call(name, dev, stream, x.data_ptr(), xt, n, ldx, *group, codes.data_ptr(),
           scales.data_ptr(), ts, lead[-1], d_in, fmt, y.data_ptr(), yt, ldy)
@@ -274,7 +278,7 @@ def _gemm(name, a_codes, a_scales, offsets, codes, scales, d_in, fmt, a_scale, b
     tb = _scale(b_scale, lead[0] if grouped else 1, fmt, "b_scale", dev)
     if grouped:
         _offsets(offsets, lead[0], dev)
-    y, yt, ldy = _output(y, codes, (n, lead[-1]), dtype)
+    y, yt, ldy = _output(y, codes, (n, lead[-1]), dtype, stream)
     group = (offsets.data_ptr(), lead[0]) if grouped else ()
     _call(name, dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), ta, n, *group,
           codes.data_ptr(), scales.data_ptr(), tb, lead[-1], d_in, fmt, y.data_ptr(), yt, ldy)
