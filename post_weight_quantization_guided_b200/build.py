@@ -31,7 +31,7 @@ def _sources():
 
 def _shared_inputs():
     """Files every translation unit depends on: the headers and this script."""
-    return (sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
+    return (sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
             + sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)])
 
 

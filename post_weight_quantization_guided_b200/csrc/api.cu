@@ -25,10 +25,17 @@ static std::atomic<long long> g_wait_limit{kDefaultWaitLimit};
 
 long long wait_limit() { return g_wait_limit.load(); }
 
+int current_device()
+{
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 int device_sm_count()
 {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
+    const int dev = current_device();
+    int sms = 0;
+    if (dev < 0)
         return 148;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
         return 148;

@@ -452,4 +452,21 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16kind(int M, int N, bool a_m
            | (static_cast<uint32_t>(M >> 4) << 24); // M / 16
 }
 
+// ------------------------------------------------------------------------------------------
+// Host helpers of the launchers
+// ------------------------------------------------------------------------------------------
+int current_device();  // -1 if there is none (api.cu)
+
+// How many clusters of a launch run at once on the current device (0 if that cannot be told, which is
+// not an error of the call that asks).
+template <typename Kernel>
+int max_active_clusters(Kernel kernel, const cudaLaunchConfig_t &cfg)
+{
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess)
+        return n;
+    (void)cudaGetLastError();
+    return 0;
+}
+
 }  // namespace lnq

@@ -36,6 +36,7 @@
 #include "common.cuh"
 #include "lnq_internal.cuh"
 #include "profile.cuh"
+#include "resident.h"
 
 namespace lnq {
 
@@ -657,17 +658,11 @@ cudaError_t fisher_syrk(const __nv_bfloat16 *X, const float *S, const float *M,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // persistent: as many pairs as can be resident at once (one CTA per SM)
-    static int resident[2] = {0, 0};
-    int &res = resident[guided ? 1 : 0];
-    if (res == 0) {
+    static ResidentClusters resident[2];
+    const int res = resident[guided ? 1 : 0].get(current_device(), num_sms / 2, [&]() {
         cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
-        int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
-            (void)cudaGetLastError();   // a failed query is not an error of this call
-            clusters = num_sms / 2;
-        }
-        res = clusters;
-    }
+        return max_active_clusters(kernel, cfg);
+    });
     int pairs = res < p.num_tiles ? res : p.num_tiles;
     if (pairs < 1)
         pairs = 1;

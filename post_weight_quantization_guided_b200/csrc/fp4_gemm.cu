@@ -38,6 +38,7 @@
 #include "fp4_mma.cuh"
 #include "lnq_internal.cuh"
 #include "profile.cuh"
+#include "resident.h"
 
 namespace lnq {
 
@@ -719,16 +720,11 @@ static cudaError_t gemm_tile(const Fp4Matrix &a, const Fp4Matrix &w, int64_t d_i
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (p.split == 1) {
-        static int resident = 0;  // pairs that run at once (one CTA per SM)
-        if (resident == 0) {
+        static ResidentClusters pairs;  // one CTA per SM
+        const int resident = pairs.get(current_device(), num_sms / 2, [&]() {
             cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
-            int clusters = 0;
-            if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
-                (void)cudaGetLastError();  // a failed query is not an error of this call
-                clusters = num_sms / 2;
-            }
-            resident = clusters;
-        }
+            return max_active_clusters(kernel, cfg);
+        });
         tiles = tiles < resident ? tiles : resident;
     }
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * 2 * p.split));

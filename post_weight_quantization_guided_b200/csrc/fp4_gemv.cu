@@ -25,10 +25,9 @@
 //
 // With few tiles several warps of a CTA share a tile's K, and where x does not fit its shared
 // memory several CTAs of a cluster do; the sums are added in order.
-#include <atomic>
-
 #include "fp4.cuh"
 #include "profile.cuh"
+#include "resident.h"
 
 namespace lnq {
 
@@ -459,25 +458,18 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
     // CTAs wait for one another.
     constexpr int64_t kWork = 62 + 13 * NT, kRound = 390, kClusterRound = 530;
     const int64_t stage = min((n + experts - 1) / experts, int64_t(NT * 8 / Pieces<TX>::n)) * Pieces<TX>::n * 4;
-    static std::atomic<int> resident[4];  // clusters that run at once, by their size
+    static ResidentClusters resident[4];  // by their size
+    const int device = current_device();
     int shares = 1, part_log = 0;
     int64_t clusters = 1, best = INT64_MAX;
     for (int i = 0, c = 1; c <= kMaxShares && (c == 1 || chunks >= c * 2); ++i, c *= 2) {
-        int room = resident[i].load(std::memory_order_relaxed);
-        if (room == 0) {
-            room = 2 * num_sms / c;
-            if (c > 1) {
-                attr[0].val.clusterDim.x = static_cast<unsigned>(c);
-                cfg.gridDim = dim3(static_cast<unsigned>(room * c));
-                cfg.dynamicSmemBytes = kXBytes / kChunkBytes * kChunkBytes;
-                int active = 0;
-                if (cudaOccupancyMaxActiveClusters(&active, kernel, &cfg) == cudaSuccess && active > 0)
-                    room = active;
-                else
-                    (void)cudaGetLastError();  // a failed query is not an error of this call
-            }
-            resident[i].store(room, std::memory_order_relaxed);
-        }
+        const int whole_sms = 2 * num_sms / c;
+        const int room = c == 1 ? whole_sms : resident[i].get(device, whole_sms, [&]() {
+            attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+            cfg.gridDim = dim3(static_cast<unsigned>(whole_sms * c));
+            cfg.dynamicSmemBytes = kXBytes / kChunkBytes * kChunkBytes;
+            return max_active_clusters(kernel, cfg);
+        });
         const int64_t own = (chunks + c - 1) / c, m = max(int64_t(1), min(tiles, room / busy));
         const int64_t per_cta = (tiles + m - 1) / m, waves = (m * busy + room - 1) / room;
         for (int k = 0; k < 4 && (k == 0 || own >= 2 << k); ++k) {

@@ -38,6 +38,7 @@
 #include "common.cuh"
 #include "lnq_internal.cuh"
 #include "profile.cuh"
+#include "resident.h"
 
 namespace lnq {
 
@@ -902,19 +903,11 @@ static cudaError_t launch_vgemm_m(const CUtensorMap &map, VgParams p, const floa
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // persistent: as many pairs as can be resident at once (at most one CTA per SM)
-    static int resident[5] = {0, 0, 0, 0, 0};
-    constexpr int slot = M == 0 ? 0 : (M == 2 ? 1 : (M == 4 ? 2 : (M == 8 ? 3 : 4)));
-    if (resident[slot] == 0) {
+    static ResidentClusters resident;
+    int pairs = resident.get(current_device(), num_sms / 2, [&]() {
         cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
-        int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, lnq_vgemm_kernel<M>, &cfg) != cudaSuccess ||
-            clusters < 1) {
-            (void)cudaGetLastError();   // a failed query is not an error of this call
-            clusters = num_sms / 2;
-        }
-        resident[slot] = clusters;
-    }
-    int pairs = resident[slot];
+        return max_active_clusters(lnq_vgemm_kernel<M>, cfg);
+    });
     if (pairs > p.num_tiles)
         pairs = p.num_tiles;
     if (pairs < 1)
