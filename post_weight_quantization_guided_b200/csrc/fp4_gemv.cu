@@ -216,7 +216,10 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
     const int left_blocks = (d_in - (chunks - 1) * kChunk - t * 32 + fp4_block(FMT) - 1) / fp4_block(FMT);
     const uint32_t tail = left_blocks >= kBlocks ? 0xFFFFu : (left_blocks == 1 ? 0xFFu : 0u);
     const int64_t first = static_cast<int64_t>(e) * d_out;
-    const float scale = (w.t == nullptr ? 1.f : __ldg(w.t + e)) * kUnshift<FMT>;
+    // the power of two goes to the sum before a large t, with which it might overflow
+    const float t_e = w.t == nullptr ? 1.f : __ldg(w.t + e);
+    const bool t_large = fabsf(t_e) >= 1.f;
+    const float scale0 = t_large ? kUnshift<FMT> : 1.f, scale1 = t_large ? t_e : t_e * kUnshift<FMT>;
     const int own = (chunks + shares - 1) / shares;  // chunks of the cluster's largest share
     const int count = (tiles - cluster + clusters - 1) / clusters;  // tiles: every clusters-th
     const bool once = c_end - c_begin <= panel;  // x fits at once
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
                 const int j = (cluster + (done + k) * clusters) * kRows + r;
                 if (b0 + b >= rows.y || j >= d_out)
                     return;
-                sum *= scale;
+                sum = sum * scale0 * scale1;
                 const int64_t o = static_cast<int64_t>(b0 + b) * ldy + j;
                 if (yt == LNQ_BF16)
                     static_cast<__nv_bfloat16 *>(y)[o] = from_f32<__nv_bfloat16>(sum);
