@@ -112,19 +112,48 @@ struct Fp4GemmParams {
     long long limit;
 };
 
+// What a finished sum v is multiplied by, one after the other: v * f2 * f0 * f1 is v * ta * tw, where
+// neither ta nor tw alone takes it out of the 32-bit range. f2 is a power of two, 1 in all ordinary
+// cases (and then left out). For the sums that there can be, 0 and 2^-20 to 2^47 (six bits a code and
+// scale, 2^24 products): f0 takes an exponent of -60 to 60, so v * f2 is inexact or infinite only where
+// the result is 0 or infinite.
+struct Fp4Factors {
+    float f0, f1, f2;
+    __device__ __forceinline__ Fp4Factors(float ta, float tw) : f0(ta), f1(tw), f2(1.f)
+    {
+        auto ordinary = [](float t) { return t >= 0x1p-60f && t <= 0x1p60f; };
+        auto valid = [](float t) { return t > 0.f && t < __uint_as_float(0x7F800000u); };
+        if ((ordinary(ta) && ordinary(tw)) || !valid(ta) || !valid(tw))
+            return;
+        int e = 0;
+        auto mantissa = [&](float t) {  // of t, 1 .. 2, its exponent added to e
+            const float n = t < 0x1p-126f ? t * 0x1p64f : t;
+            e += static_cast<int>(__float_as_uint(n) >> 23) - 127 - (t < 0x1p-126f ? 64 : 0);
+            return __uint_as_float((__float_as_uint(n) & 0x007FFFFFu) | 0x3F800000u);
+        };
+        f0 = mantissa(ta);
+        f1 = mantissa(tw);
+        const int near = max(-60, min(e, 60)), rest = min(e - near, 127);  // 2^127 is infinite already
+        f0 *= __uint_as_float(static_cast<uint32_t>(near + 127) << 23);
+        f2 = __uint_as_float(rest >= -126 ? static_cast<uint32_t>(rest + 127) << 23
+                                          : (rest >= -149 ? 1u << (rest + 149) : 0u));
+    }
+    __device__ __forceinline__ float operator()(float v) const { return v * f0 * f1; }
+};
+
 template <typename T>
 __device__ __forceinline__ void store_column(T *__restrict__ y, int64_t ldy, int count,
-                                             const uint32_t (&v)[32], float ta, float tw)
+                                             const uint32_t (&v)[32], const Fp4Factors &f)
 {
     if (count >= 32) {
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-            y[c * ldy] = from_f32<T>(__uint_as_float(v[c]) * ta * tw);
+            y[c * ldy] = from_f32<T>(f(__uint_as_float(v[c])));
     } else {
 #pragma unroll
         for (int c = 0; c < 32; ++c)
             if (c < count)
-                y[c * ldy] = from_f32<T>(__uint_as_float(v[c]) * ta * tw);
+                y[c * ldy] = from_f32<T>(f(__uint_as_float(v[c])));
     }
 }
 
@@ -581,7 +610,14 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
             const int j = at.j0 + static_cast<int>(cr) * BM + quarter * 32 + lane;
             if (j >= p.d_out)
                 continue;
-            const float tw = p.tw == nullptr ? 1.f : __ldg(p.tw + at.e);
+            const Fp4Factors f(ta, p.tw == nullptr ? 1.f : __ldg(p.tw + at.e));
+            if (f.f2 != 1.f) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        v[c][k] = __float_as_uint(__uint_as_float(v[c][k]) * f.f2);
+            }
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 const int col = (2 * c + half) * 32, count = rows - col;
@@ -589,11 +625,11 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                     continue;
                 const int64_t o = static_cast<int64_t>(at.b0 + col) * p.ldy + j;
                 if (p.yt == LNQ_BF16)
-                    store_column(static_cast<__nv_bfloat16 *>(p.y) + o, p.ldy, count, v[c], ta, tw);
+                    store_column(static_cast<__nv_bfloat16 *>(p.y) + o, p.ldy, count, v[c], f);
                 else if (p.yt == LNQ_F16)
-                    store_column(static_cast<__half *>(p.y) + o, p.ldy, count, v[c], ta, tw);
+                    store_column(static_cast<__half *>(p.y) + o, p.ldy, count, v[c], f);
                 else
-                    store_column(static_cast<float *>(p.y) + o, p.ldy, count, v[c], ta, tw);
+                    store_column(static_cast<float *>(p.y) + o, p.ldy, count, v[c], f);
             }
         }
     }
@@ -607,8 +643,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
         const Fp4TileAt at = tile_at<BN>(first, p, lim, pre);
         const int rows = min(at.b1 - at.b0, BN);
         const int r0 = part * rows / p.split, r1 = (part + 1) * rows / p.split;
-        const float ta = p.ta == nullptr ? 1.f : __ldg(p.ta);
-        const float tw = p.tw == nullptr ? 1.f : __ldg(p.tw + at.e);
+        const Fp4Factors f(p.ta == nullptr ? 1.f : __ldg(p.ta), p.tw == nullptr ? 1.f : __ldg(p.tw + at.e));
         uint32_t peer[kMaxSplit];
 #pragma unroll
         for (int s = 0; s < kMaxSplit; ++s)
@@ -632,7 +667,7 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
                 for (int s = 1; s < kMaxSplit; ++s)
                     if (s < p.split)
                         sum += u[s][k];
-                sum = sum * ta * tw;
+                sum = f(sum * f.f2);
                 if (j + k >= p.d_out)
                     break;
                 if (p.yt == LNQ_BF16)

@@ -47,3 +47,32 @@ def test_gemv_at_every_matrix_scale(lnq, dtype, log_t):
     y = lnq.lnq_fp4_grouped_gemv(xt, off, dev(np.stack([codes, codes])), dev(np.stack([scales, scales])),
                                  NV, tensor_scale=torch.cat([t, t]), dtype=torch.float32)
     np.testing.assert_array_equal(y.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("n,d_in", [(20, 200), (20, 1024), (300, 300), (600, 520)])
+@pytest.mark.parametrize("log_a,log_w", [
+    (0, 0), (100, -100), (-100, 100), (127, -127), (-127, 127), (-149, 127), (127, -149), (-140, 120),
+    (120, -110), (-110, 120), (60, 60), (63, 50), (-60, -50), (127, 0), (0, -120), (-130, 10),
+    (-100, -40), (-149, -149), (127, 127)])
+def test_gemm_at_every_pair_of_matrix_scales(lnq, n, d_in, log_a, log_w):
+    """Whatever the product of the sum with one of the two scales would be: sums below 2^13 in steps
+    of 1/8, which are 32-bit numbers after the scales too, or too large for them (infinite), or for
+    (-149, -149) too small (zero)."""
+    rng = np.random.default_rng([8, n, d_in])
+    d_out = 150
+    ac, as_ = ref.random_stored(rng, (n,), d_in, NV, True)
+    ac &= 0x33
+    as_[:] = 56
+    wc, ws = ref.random_stored(rng, (d_out,), d_in, NV, True)
+    total = ref.values(ac, as_, d_in, NV) @ ref.values(wc, ws, d_in, NV).T
+    assert np.abs(total).max() < 2 ** 13
+    with np.errstate(over="ignore", under="ignore"):
+        want = (total * 2.0 ** (log_a + log_w)).astype(np.float32).astype(np.float64)
+    ta, tw = [torch.tensor([2.0 ** v], dtype=torch.float32, device="cuda") for v in (log_a, log_w)]
+    a = [dev(v) for v in (ac, as_, wc, ws)]
+    y = lnq.lnq_fp4_gemm(*a, d_in, NV, a_scale=ta, b_scale=tw, dtype=torch.float32)
+    np.testing.assert_array_equal(y.double().cpu().numpy(), want)
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    y = lnq.lnq_fp4_grouped_gemm(a[0], a[1], off, a[2][None], a[3][None], d_in, NV, a_scale=ta, b_scale=tw,
+                                 dtype=torch.float32)
+    np.testing.assert_array_equal(y.double().cpu().numpy(), want)
