@@ -168,9 +168,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank()
     return r;
 }
 
-// All threads of every CTA of the cluster.
+// All threads of every CTA of the cluster. The barrier's aligned form wants whole warps, which a loop
+// or branch of single lanes before it does not promise.
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -638,7 +638,6 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
         // One tile per cluster. Each pair adds and writes its share of the rows, over the pairs
         // in order. (After a wait that gave up they may add anything: nothing is being copied to the
         // stages any more, and the call is reported.)
-        __syncwarp();
         cluster_sync();
         const Fp4TileAt at = tile_at<BN>(first, p, lim, pre);
         const int rows = min(at.b1 - at.b0, BN);
@@ -683,7 +682,6 @@ __global__ void __launch_bounds__(f4::kThreads, 1)
     // All CTAs stay until the cluster is done: the MMAs read both CTAs' shared memory, barriers
     // in the leader are signalled by both, partial sums are read by all.
     tc_fence_before();
-    __syncwarp();
     cluster_sync();
     tc_fence_after();
     if (warp == kMmaWarp)

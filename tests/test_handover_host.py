@@ -24,3 +24,17 @@ def test_arrivals_on_other_ctas_barriers_release_at_cluster_scope():
                 relaxed = ".relaxed.cluster." in op.group() and any(f in asm[:op.start()] for f in FENCES)
                 assert ".release.cluster." in op.group() or relaxed, (os.path.basename(path), asm)
     assert found, "no cluster product found"
+
+
+def test_aligned_cluster_barriers_stand_behind_a_whole_warp():
+    """The aligned form of the cluster barrier is undefined for part of a warp: nothing but the
+    helper that first brings the warp together issues it."""
+    found = 0
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu*"))):
+        text = open(path).read()
+        for m in re.finditer(r"barrier\.cluster\.arrive[\w.]*\.aligned", text):
+            found += 1
+            before = text[:m.start()].rstrip().splitlines()
+            statements = [line.strip() for line in before if not line.strip().startswith("//")]
+            assert statements[-2] == "__syncwarp();", (os.path.basename(path), statements[-2:])
+    assert found, "no cluster barrier found"
