@@ -320,15 +320,13 @@ __device__ __forceinline__ void fisher_syrk_body(const CUtensorMap &amap, const 
                     }
                 }
             }
-            if (!ok) {
-                // let this CTA's copies land before it exits: wait for the last armed phase of
-                // every stage (its parity is that of the number of completed uses)
-                for (int s = 0; s < STAGES; ++s) {
-                    if (!((used >> s) & 1u))
-                        continue;
-                    const int last_use = s < stage ? use : use - 1;
-                    mbar_wait(&raw_full[s], last_use & 1, kDrainLimit);
-                }
+            // this CTA's copies land before it exits, whichever wait gave up: wait for the last armed
+            // phase of every stage (its parity is that of the number of completed uses)
+            for (int s = 0; s < STAGES; ++s) {
+                if (!((used >> s) & 1u))
+                    continue;
+                const int last_use = s < stage ? use : use - 1;
+                mbar_wait(&raw_full[s], last_use & 1, kDrainLimit);
             }
         }
     } else if (warp == 0) {
@@ -365,18 +363,16 @@ __device__ __forceinline__ void fisher_syrk_body(const CUtensorMap &amap, const 
                     stage = (stage + 1 == STAGES) ? 0 : stage + 1;
                 }
             }
+            // The copies land before the pair exits, whichever wait gave up: the even CTA waits for
+            // the last phase of each stage it armed, which counts both CTAs' copies. Where one of the
+            // CTAs gave up loading, the other may have copies that no armed phase counts: a fixed time.
+            if (cr == 0)
+                for (int s = 0; s < STAGES; ++s)
+                    if ((fused >> s) & 1u)
+                        mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, kPairDrainLimit);
             if (!ok) {
-                // let this CTA's copies land before the pair exits: the even CTA waits for the
-                // last phase of each stage it armed; the odd CTA's copies are counted there, so it
-                // waits a fixed time
-                if (cr == 0) {
-                    for (int s = 0; s < STAGES; ++s)
-                        if ((fused >> s) & 1u)
-                            mbar_wait(&full[s], ((fpar >> s) & 1u) ^ 1u, kPairDrainLimit);
-                } else {
-                    const long long c0 = clock64();
-                    while (clock64() - c0 < kPairDrainLimit) {
-                    }
+                const long long c0 = clock64();
+                while (clock64() - c0 < kPairDrainLimit) {
                 }
             }
         }

@@ -348,15 +348,14 @@ __global__ void __launch_bounds__(sw::NUM_THREADS, 1)
                 }
                 mbar_arrive(bs_free);
             }
-            if (!ok) {
-                // the last fill of slot s completed phase (fills - 1), parity = fills parity ^ 1
-                for (int s = 0; s < NA; ++s)
-                    if ((aused >> s) & 1u)
-                        mbar_wait(&a_full[s], ((apar >> s) & 1u) ^ 1u, kDrainLimit);
-                for (int s = 0; s < NH; ++s)
-                    if ((hused >> s) & 1u)
-                        mbar_wait(&h_full[s], ((hpar >> s) & 1u) ^ 1u, kDrainLimit);
-            }
+            // All copies land, whichever wait gave up: the last fill of slot s completes phase
+            // (fills - 1), parity = fills parity ^ 1.
+            for (int s = 0; s < NA; ++s)
+                if ((aused >> s) & 1u)
+                    mbar_wait(&a_full[s], ((apar >> s) & 1u) ^ 1u, kDrainLimit);
+            for (int s = 0; s < NH; ++s)
+                if ((hused >> s) & 1u)
+                    mbar_wait(&h_full[s], ((hpar >> s) & 1u) ^ 1u, kDrainLimit);
             bulk_wait_all();
         }
     } else if (warp == 1) {

@@ -439,21 +439,20 @@ __global__ void __launch_bounds__(vg::NUM_THREADS, 1)
                     }
                 }
             }
+            // The copies land before the pair exits, whichever wait gave up: the even CTA waits for
+            // the last phase of each slot it armed, which counts both CTAs' copies. Where one of the
+            // CTAs gave up loading, the other may have copies that no armed phase counts: a fixed time.
+            if (cr == 0) {
+                for (int s = 0; s < NSLOT; ++s)
+                    if ((aused >> s) & 1u)
+                        mbar_wait(&a_full[s], ((apar >> s) & 1u) ^ 1u, kPairDrainLimit);
+                for (int s = 0; s < B_STAGES; ++s)
+                    if ((bused >> s) & 1u)
+                        mbar_wait(&b_full[s], ((bpar >> s) & 1u) ^ 1u, kPairDrainLimit);
+            }
             if (!ok) {
-                // let this CTA's copies land before the pair exits: the even CTA waits for the last
-                // phase of each slot it armed; the odd CTA's copies are counted there, so it waits
-                // a fixed time
-                if (cr == 0) {
-                    for (int s = 0; s < NSLOT; ++s)
-                        if ((aused >> s) & 1u)
-                            mbar_wait(&a_full[s], ((apar >> s) & 1u) ^ 1u, kPairDrainLimit);
-                    for (int s = 0; s < B_STAGES; ++s)
-                        if ((bused >> s) & 1u)
-                            mbar_wait(&b_full[s], ((bpar >> s) & 1u) ^ 1u, kPairDrainLimit);
-                } else {
-                    const long long t0 = clock64();
-                    while (clock64() - t0 < kPairDrainLimit) {
-                    }
+                const long long t0 = clock64();
+                while (clock64() - t0 < kPairDrainLimit) {
                 }
             }
         }
