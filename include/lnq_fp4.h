@@ -89,15 +89,18 @@ LNQ_API lnq_status lnq_fp4_dequantize(const uint8_t *codes, const uint8_t *scale
  * for the few rows of a decoding step (any nb >= 0 is taken; the weights are read once for every
  * 32 rows of bf16, 16 of f16 or 10 of f32 x, and lnq_fp4_gemm is the operator for prompts).
  *   x [nb][ldx] of type xt; codes, scales [d_out] rows of d_in; y [nb][ldy] of type yt, out.
- * Arithmetic: every product is exact (bits of a 32-bit x below 2^-133 may be dropped), the sums
- * are 32-bit, t multiplies the finished sum, and y is rounded once to its type. */
+ * Arithmetic: every product is exact, the sums are 32-bit, the product of t with the finished sum is
+ * rounded to 32 bits and then to y's type. (Bits of a 32-bit x below 2^-133, and of a product before t
+ * below 2^-142, may be dropped.) */
 LNQ_API lnq_status lnq_fp4_gemv(const void *x, lnq_dtype xt, int64_t nb, int64_t ldx,
                                 const uint8_t *codes, const uint8_t *scales, const float *t,
                                 int64_t d_out, int64_t d_in, lnq_fp4_format fmt, void *y,
                                 lnq_dtype yt, int64_t ldy, lnq_stream_t stream);
 
 /* lnq_fp4_gemv with the rows of x grouped by expert: codes and scales hold `experts` matrices of
- * d_out rows one after another, t is [experts] (or NULL). */
+ * d_out rows one after another, t is [experts] (or NULL). A pass over a matrix takes the rows of an
+ * average group (n / experts, rounded up to 8, 16, 24 or 32 rows of bf16, half of that of f16, 2, 5, 8
+ * or 10 of f32); a larger group reads its matrix once for each such number of rows. */
 LNQ_API lnq_status lnq_fp4_grouped_gemv(const void *x, lnq_dtype xt, int64_t n, int64_t ldx,
                                         const int32_t *offsets, int64_t experts,
                                         const uint8_t *codes, const uint8_t *scales,
@@ -109,8 +112,9 @@ LNQ_API lnq_status lnq_fp4_grouped_gemv(const void *x, lnq_dtype xt, int64_t n, 
  * block-scaled tensor cores.
  *   a: codes and scales of [n] rows of d_in, matrix scale ta; w: of [d_out] rows, matrix scale
  *   tw; y [n][ldy] of type yt, out.
- * Arithmetic: products of codes and block scales are exact, the sums 32-bit; ta and tw multiply
- * the finished sum, which is rounded once to yt. */
+ * Arithmetic: products of codes and block scales are exact, the sums 32-bit (24 bits, cut off); ta
+ * and tw multiply the finished sum, each product rounded to 32 bits and the last one to yt. Where
+ * the sum times one of them would leave the 32-bit range and the result does not, nothing is lost. */
 LNQ_API lnq_status lnq_fp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, const float *ta,
                                 int64_t n, const uint8_t *w_codes, const uint8_t *w_scales,
                                 const float *tw, int64_t d_out, int64_t d_in,

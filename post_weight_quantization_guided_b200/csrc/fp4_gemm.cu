@@ -25,13 +25,18 @@
 // With few tiles, two pairs of one cluster take half of K each and add their sums through
 // distributed shared memory in a fixed order.
 //
-// What bounds it. Many rows: shared memory. A stage moves about 88 KB of it per CTA (codes written
-// and read 64, scales written, rearranged twice and copied to TMEM 24), 690 cycles at 128 bytes a
-// cycle where the MMAs take 512. One B200, 16384 x 4096 -> 14336 NV: 390 to 410 us (4.7 to 4.9
-// PFLOP/s, tensor pipe active 51% of the time) at the clock that the power limit leaves; without its
-// code loads 295 us, without its stores 350, without tcgen05.cp 360. (256-row tiles of two accumulators
-// do not fit TMEM beside the scales; stores through shared memory in 16-byte pieces were no faster.)
-// Few rows: the weights' bytes, after 3 us to the first stage: 32 x 4096 -> 14336 10 us in the kernel.
+// What bounds it: the way from stage to stage. One B200, operands in L2: a stage takes 0.36 to 0.38 us
+// (about 700 cycles; the slope of the time from K = 4096 to 16384), in 64-row tiles, whose MMAs take
+// 128 cycles, as in 256-row ones, whose MMAs take 512, and with 4 pairs at work as with 32. Neither
+// the tensor core nor memory sets that pace, nor shared memory (88 KB a stage and CTA in 256-row
+// tiles, 690 cycles at 128 bytes a cycle, but 56 KB in 64-row ones), but the chain of TMA, rearranging
+// warp, fence, arrival, copy to TMEM, MMA and commit over rings of this depth. With all 74 pairs at
+// work it is 0.39 to 0.45 us from L2 and, of operands that L2 does not hold, 0.52 to 0.61.
+// 16384 x 4096 -> 14336 NV: 418 us (4.6 PFLOP/s) at the clock that the power limit leaves; at an earlier
+// 389 us it was 295 without its code loads, 350 without its stores, 360 without tcgen05.cp. (256-row
+// tiles of two accumulators do not fit TMEM beside the scales; stores through shared memory in
+// 16-byte pieces were no faster.)
+// Few rows: 3 us to the first stage, a tile's stages, the last stores: 32 x 4096 -> 14336 13.5 us.
 #include <cstring>
 
 #include "fp4.cuh"

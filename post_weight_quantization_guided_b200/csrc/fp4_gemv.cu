@@ -4,9 +4,12 @@
 //   y[b][j] = t sum_k s[j][k] sum_{i in block k} x[b][i] code[j][i]
 //
 // Bound: HBM, the codes and scales read once (half a byte and 1/16 (NV) or 1/32 (MX) of a byte an
-// element); in practice the decoding, about 3.4 instructions an element (integer pipe 57% busy). One
-// B200: 16 rows over 8 experts 4096 -> 14336 73 us (3.6 TB/s of codes and scales), 1 x 4096 -> 14336
-// 14 us, 1 x 4096 -> 4096 8.3 us, 7 x 11008 -> 4101 in 32 bits 22 us.
+// element). Large calls take instructions instead, about 3.4 an element: 16 rows over 8 experts 4096 ->
+// 14336 75 us (3.5 TB/s of codes and scales), no unit full over the whole kernel (issue slots 67%,
+// integer pipe 60%), but more than one warp ready where one issues. Small ones take their fixed
+// parts, one after the other (x to shared memory, decoding, the join), and a last round of tiles that
+// does not fill the warps: 1 x 4096 -> 14336 16 us, 16 x 4096 -> 14336 29 us, 1 x 4096 -> 4096 8.7 us,
+// 7 x 11008 -> 4101 in 32 bits 22 us.
 //
 // The products run on mma.sync m16n8k16 in bf16 with 32-bit sums: with at most a few rows the
 // work is decoding weights, and the instruction takes them straight from registers, where
@@ -150,7 +153,7 @@ struct Chunk {
 };
 
 // Weights enter as code * s * 2^kShift. NV: s 2^119 is a normal number for every s. MX: with a factor
-// 2^-2 every code * s is a bf16 number (6 2^127 2^-2 .. 0.5 2^-127 2^-2, the smallest subnormal), and
+// 2^-2 every code * s is a bf16 number (6 2^127 2^-2 .. 0.5 2^-127 2^-2 = 2^-130, a subnormal one), and
 // its multiplier 2^(v - 127 + 124) one while v <= kTopScale; a larger v takes a second factor.
 template <int FMT> constexpr float kUnshift = FMT == LNQ_FP4_MX ? 4.f : 128.f;
 constexpr uint32_t kTopScale = 130u;
@@ -196,8 +199,8 @@ __global__ void __launch_bounds__(gv::kThreads, 2)
     // x: a word's 8 columns by 4 lanes t in the order of the lanes that read them
     extern __shared__ uint4 xs[];  // [panel][NT][4 words][8 columns][4 lanes t]
     __shared__ float sums[kWarps][NT * 8][kSumPitch];
-    // the multiplier of each scale byte (83 us where computing them takes 87, 16 rows over 8 experts
-    // 4096 -> 14336; 37 and 39, 10 rows in 32 bits)
+    // the multiplier of each scale byte (76 us where computing them takes 80, 16 rows over 8 experts
+    // 4096 -> 14336; 117 and 121, 64 rows; the same where there is one matrix)
     __shared__ uint32_t multiplier[256];
     const int e = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -455,10 +458,13 @@ static cudaError_t gemv_tiles(const void *x, int n, int64_t ldx, const int32_t *
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // How K is shared: by `shares` CTAs of a cluster (less of x for each to write) and 2^`part_log`
-    // warps of a CTA. The least time, in units of 6.5 ns, fitted to 15 sizes at all shares and parts,
-    // two CTAs an SM (it picks the fastest at each or one within 1% of it): a chunk of a column of x
-    // staged, a chunk of a tile, and a round's fixed costs, which are larger where a cluster's
-    // CTAs wait for one another.
+    // warps of a CTA. The least cost: a chunk of a column of x staged, a chunk of a tile, and a
+    // round's fixed costs, which are larger where a cluster's CTAs wait for one another. The weights
+    // were fitted to measured times and rank plans; they do not tell the time (from cold caches
+    // 1.2 to 5 times 6.5 ns a unit). Against all shares and parts at 16 sizes (1 to 64 rows, bf16, fp16
+    // and fp32, 2048 .. 11008 -> 1408 .. 14336, 1 to 64 experts) it takes the fastest plan or one within
+    // 2% of it at 14, 4% more at 16 x 4096 -> 14336 bf16 (33 us where four CTAs to a tile take 32) and 6%
+    // at 4 x 2048 -> 1408 fp32 (12.3, 11.6).
     constexpr int64_t kWork = 62 + 13 * NT, kRound = 390, kClusterRound = 530;
     const int64_t stage = min((n + experts - 1) / experts, int64_t(NT * 8 / Pieces<TX>::n)) * Pieces<TX>::n * 4;
     static ResidentClusters resident[4];  // by their size

@@ -5,9 +5,12 @@
 //
 // Bound: HBM (read x, write half a byte an element). One pass: a lane takes 16 consecutive
 // elements, an NV block or half an MX one (whose two lanes agree on its largest element by a
-// shuffle), a warp 512 elements of a row. One B200, 16384 x 4096 bf16: MX 31 us (the bytes alone 26 at
-// the copy rate), NV 41 to 53 us by how many ties t makes, reading back 37 us, the matrix scale
-// 29 us; 4096 x 11008 f32: 37 us either way.
+// shuffle), a warp 512 elements of a row. One B200, 16384 x 4096 bf16: MX 28 us (the bytes alone 26 at
+// the copy rate), NV 37 to 40 us (a span is loaded and then worked on, with nothing in flight
+// meanwhile: issue slots 60 to 65% busy, integer pipe 51 to 56%, DRAM 27%), reading back 34 us, the matrix
+// scale 24.5 and 2 for its quotient; 4096 x 11008 f32: 34 to 38, reading back 36, the scale 32.
+// Rows whose pitch is no multiple of 16 bytes go element by element: 16384 x 4095 bf16 takes 71
+// (MX) and 73 us, reading back 206, the scale 74; 4096 x 11007 f32 96 (MX) and 88, 67, 85.
 //
 // Exact decisions. MX quotients are exact (a power of two). An NV quotient is estimated in 32 bits
 // and rounded twice, a little below and a little above the estimate; where both agree that is the
